@@ -7,14 +7,16 @@ output tensors.  There is no CPU fallback: if the library is missing the
 import of the functions below raises.
 
 The ``qfp4_*`` functions mirror the C entry points one to one (pointers as
-integers); ``quantize``, ``quantize_mxfp8``, ``dequantize``, ``gemm`` and
-``gemm_fused_rq`` are conveniences that allocate outputs.
+integers); ``quantize``, ``quantize_mxfp8``, ``dequantize``, ``gemm``,
+``gemm_fused_rq``, ``gemm_epilogue``, ``linear_forward_epilogue``,
+``epilogue_backward``, ``dropout``, ``layernorm_forward`` and
+``layernorm_backward`` are conveniences that allocate outputs.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_int, c_int64, c_size_t, c_uint64, c_void_p, c_char_p
+from ctypes import c_int, c_int64, c_size_t, c_uint64, c_void_p, c_char_p, c_double, c_float
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqfp4.so")
@@ -24,6 +26,7 @@ RNE, SR = 0, 1
 BF16, F32 = 0, 1
 GRAN_TENSOR, GRAN_ROW, GRAN_GROUP16, GRAN_GROUP32 = 0, 1, 2, 3
 SCALE_DEFAULT, SCALE_OCP_FLOOR, SCALE_E4M3_UP = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 OK, ERR_ARG, ERR_SHAPE, ERR_UNSUPPORTED, ERR_ALIGN, ERR_CUDA, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5, -6
 DEV_ERR_TIMEOUT = 1
 
@@ -32,12 +35,22 @@ EXPORTS = [
     "qfp4_dequantize", "qfp4_gemm_workspace_bytes", "qfp4_gemm_blockscaled", "qfp4_gemm_fused_rq_workspace_bytes",
     "qfp4_gemm_fused_rq", "qfp4_gemm_fused_rq_ex", "qfp4_gemm_fused_rq_workspace_layout", "qfp4_gemm_blockscaled_noalloc",
     "qfp4_linear_forward_workspace_bytes", "qfp4_linear_forward", "qfp4_linear_backward_workspace_bytes",
-    "qfp4_linear_backward", "qfp4_kl_calibrate_workspace_bytes", "qfp4_kl_calibrate",
+    "qfp4_linear_backward", "qfp4_gemm_epilogue_workspace_bytes", "qfp4_gemm_epilogue",
+    "qfp4_linear_forward_epilogue", "qfp4_epilogue_backward_workspace_bytes", "qfp4_epilogue_backward",
+    "qfp4_dropout", "qfp4_layernorm_forward", "qfp4_layernorm_backward_workspace_bytes", "qfp4_layernorm_backward",
+    "qfp4_kl_calibrate_workspace_bytes", "qfp4_kl_calibrate",
     "qfp4_status_string", "qfp4_last_device_error", "qfp4_selftest_wait_timeout", "qfp4_version",
     "qfp4_launch_count",
 ]
 
 _lib = None
+
+
+class Epilogue(ctypes.Structure):
+    """The C struct qfp4_epilogue (pointers as integers, or None)."""
+    _fields_ = [("bias", c_void_p), ("residual", c_void_p), ("preact", c_void_p), ("step", c_void_p),
+                ("seed", c_uint64), ("dropout_p", c_double), ("bias_dt", c_int), ("residual_dt", c_int),
+                ("act", c_int)]
 
 
 class QFP4Error(RuntimeError):
@@ -95,6 +108,27 @@ def lib():
         L.qfp4_linear_backward.restype = c_int
         L.qfp4_linear_backward.argtypes = [P, P, P, c_int64, c_int64, c_int64, c_int, c_uint64, c_int, P, P, P,
                                            c_size_t, P]
+        L.qfp4_gemm_epilogue_workspace_bytes.restype = c_size_t
+        L.qfp4_gemm_epilogue_workspace_bytes.argtypes = [c_int64, c_int64, c_int64, c_int]
+        L.qfp4_gemm_epilogue.restype = c_int
+        L.qfp4_gemm_epilogue.argtypes = [P, P, P, P, P, P, c_int64, c_int64, c_int64, c_int, P, c_int, P, P, c_size_t,
+                                         P]
+        L.qfp4_linear_forward_epilogue.restype = c_int
+        L.qfp4_linear_forward_epilogue.argtypes = [P, P, c_int64, c_int64, c_int64, c_int, c_int, P, c_int, P, P,
+                                                   c_size_t, P]
+        L.qfp4_epilogue_backward_workspace_bytes.restype = c_size_t
+        L.qfp4_epilogue_backward_workspace_bytes.argtypes = [c_int64, c_int64]
+        L.qfp4_epilogue_backward.restype = c_int
+        L.qfp4_epilogue_backward.argtypes = [P, P, c_int, c_int64, c_int64, c_int, c_double, c_uint64, P, P, P, P,
+                                             c_size_t, P]
+        L.qfp4_dropout.restype = c_int
+        L.qfp4_dropout.argtypes = [P, c_int, c_int64, c_double, c_uint64, P, P, P, P]
+        L.qfp4_layernorm_forward.restype = c_int
+        L.qfp4_layernorm_forward.argtypes = [P, c_int, c_int64, c_int64, P, P, c_int, c_float, P, P, P, P]
+        L.qfp4_layernorm_backward_workspace_bytes.restype = c_size_t
+        L.qfp4_layernorm_backward_workspace_bytes.argtypes = [c_int64, c_int64]
+        L.qfp4_layernorm_backward.restype = c_int
+        L.qfp4_layernorm_backward.argtypes = [P, P, c_int, c_int64, c_int64, P, c_int, P, P, P, P, P, P, c_size_t, P]
         L.qfp4_kl_calibrate_workspace_bytes.restype = c_size_t
         L.qfp4_kl_calibrate_workspace_bytes.argtypes = [c_int, c_int, c_int]
         L.qfp4_kl_calibrate.restype = c_int
@@ -206,6 +240,54 @@ def qfp4_linear_backward_workspace_bytes(M, N, K, fmt):
 def qfp4_linear_backward(G, X, W, M, N, K, fmt, seed, out_dt, dX, dW, workspace, workspace_bytes, stream):
     return lib().qfp4_linear_backward(G, X, W, M, N, K, fmt, seed & ((1 << 64) - 1), out_dt, dX, dW, workspace,
                                       workspace_bytes, stream)
+
+
+def qfp4_gemm_epilogue_workspace_bytes(M, N, K, fmt):
+    return lib().qfp4_gemm_epilogue_workspace_bytes(M, N, K, fmt)
+
+
+def _epilogue_ref(epilogue):
+    return None if epilogue is None else ctypes.addressof(epilogue)
+
+
+def qfp4_gemm_epilogue(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, epilogue, out_dt, out,
+                       workspace, workspace_bytes, stream):
+    """epilogue: an ``Epilogue``, or None."""
+    return lib().qfp4_gemm_epilogue(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt,
+                                    _epilogue_ref(epilogue), out_dt, out, workspace, workspace_bytes, stream)
+
+
+def qfp4_linear_forward_epilogue(X, W, M, N, K, fmt, four6, epilogue, out_dt, Y, workspace, workspace_bytes, stream):
+    """epilogue: an ``Epilogue``, or None."""
+    return lib().qfp4_linear_forward_epilogue(X, W, M, N, K, fmt, four6, _epilogue_ref(epilogue), out_dt, Y,
+                                              workspace, workspace_bytes, stream)
+
+
+def qfp4_epilogue_backward_workspace_bytes(M, N):
+    return lib().qfp4_epilogue_backward_workspace_bytes(M, N)
+
+
+def qfp4_epilogue_backward(dY, Z, dt, M, N, act, dropout_p, seed, step, dZ, dbias, workspace, workspace_bytes, stream):
+    return lib().qfp4_epilogue_backward(dY, Z, dt, M, N, act, dropout_p, seed & ((1 << 64) - 1), step, dZ, dbias,
+                                        workspace, workspace_bytes, stream)
+
+
+def qfp4_dropout(x, dt, n, p, seed, step, residual, out, stream):
+    return lib().qfp4_dropout(x, dt, n, p, seed & ((1 << 64) - 1), step, residual, out, stream)
+
+
+def qfp4_layernorm_forward(x, dt, M, D, gamma, beta, wdt, eps, y, mean, rstd, stream):
+    return lib().qfp4_layernorm_forward(x, dt, M, D, gamma, beta, wdt, eps, y, mean, rstd, stream)
+
+
+def qfp4_layernorm_backward_workspace_bytes(M, D):
+    return lib().qfp4_layernorm_backward_workspace_bytes(M, D)
+
+
+def qfp4_layernorm_backward(dy, x, dt, M, D, gamma, wdt, mean, rstd, dx, dgamma, dbeta, workspace, workspace_bytes,
+                            stream):
+    return lib().qfp4_layernorm_backward(dy, x, dt, M, D, gamma, wdt, mean, rstd, dx, dgamma, dbeta, workspace,
+                                         workspace_bytes, stream)
 
 
 def qfp4_kl_calibrate_workspace_bytes(bins, levels, grid):
@@ -438,6 +520,281 @@ def linear_backward(G, X, W, fmt=NVFP4, seed=0, out_dtype=None, want_dx=True, wa
                               _ptr(o.get("dX")), _ptr(o.get("dW")), _ptr(workspace), wsb, _stream(stream))
     _check(st, "qfp4_linear_backward")
     return o.get("dX"), o.get("dW")
+
+
+# ------------------------------------------------------------------ around a linear layer
+def _tensor(t, name, like, shape=None, dtype=None):
+    """Checks of a tensor that goes to the C ABI beside `like`: CUDA,
+    contiguous, on the same device, and of the given shape and dtype."""
+    _input(t, name, dims=None)
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, not {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _param_dt(t, name):
+    torch = _torch()
+    if t is None or t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError(f"{name} must be bfloat16 or float32")
+
+
+def _step(step, like):
+    """The dropout's step counter: None, or a one-element int64 CUDA tensor."""
+    if step is None:
+        return None
+    _tensor(step, "step", like, dtype=_torch().int64)
+    if step.numel() != 1:
+        raise ValueError("step must have one element")
+    return step.data_ptr()
+
+
+class _launch_on:
+    """Runs a call on `like`'s device (the C ABI launches on the current one)
+    and on `stream` there (default: that device's current stream), as an
+    integer handle."""
+
+    def __init__(self, like, stream):
+        torch = _torch()
+        self._guard = None
+        if like.device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(like.device)
+        self._like, self._stream = like, stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        if self._stream is None:
+            return _torch().cuda.current_stream().cuda_stream
+        return self._stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _new(shape, dtype, like, stream):
+    """A fresh tensor on `like`'s device, of the allocator's pool for the
+    stream that the call runs on (its memory may still be in use elsewhere
+    on any other)."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _operand(q, name, rows, K, fmt, like):
+    torch = _torch()
+    g = 16 if fmt == NVFP4 else 32
+    _tensor(q["codes"], f"{name} codes", like, (rows, K if fmt == MXFP8 else K // 2), torch.uint8)
+    _tensor(q["scales"], f"{name} scales", like, (rows, K // g), torch.uint8)
+    if fmt == NVFP4:
+        _tensor(q["tscale"], f"{name} tscale", like, dtype=torch.float32)
+
+
+def _epilogue(M, N, out, bias, act, want_preact, dropout_p, seed, step, residual, stream):
+    """(Epilogue struct, preact tensor or None) for outputs like `out`."""
+    e = Epilogue()
+    e.act = act
+    if bias is not None:
+        _tensor(bias, "bias", out, (N,))
+        e.bias, e.bias_dt = bias.data_ptr(), _param_dt(bias, "bias")
+    if residual is not None:
+        _tensor(residual, "residual", out, (M, N))
+        e.residual, e.residual_dt = residual.data_ptr(), _param_dt(residual, "residual")
+    preact = None
+    if want_preact is not False and want_preact is not None:
+        preact = _new((M, N), out.dtype, out, stream) if want_preact is True else want_preact
+        _tensor(preact, "preact", out, (M, N), out.dtype)
+        e.preact = preact.data_ptr()
+    e.dropout_p, e.seed, e.step = dropout_p, seed & ((1 << 64) - 1), _step(step, out)
+    return e, preact
+
+
+def _out_dt(out):
+    """The C type of an output tensor."""
+    torch = _torch()
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("outputs are bfloat16 or float32")
+    return F32 if out.dtype == torch.float32 else BF16
+
+
+def gemm_epilogue(A, B, M, N, K, fmt, bias=None, act=ACT_NONE, want_preact=False, dropout_p=0.0, seed=0, step=None,
+                  residual=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """(Y, preact) with Y = residual + dropout(act(deq(A) deq(B)^T + bias)) in
+    one GEMM (qfp4_gemm_epilogue), for operands as returned by ``quantize`` or
+    ``quantize_mxfp8``.  ``want_preact``: True (or a buffer) to keep the sum
+    before the activation for ``epilogue_backward``, else preact is None.
+    ``step``: a one-element int64 CUDA tensor, the dropout's counter."""
+    torch = _torch()
+    like = B["codes"]
+    _operand(A, "A", M, K, fmt, like)
+    _operand(B, "B", N, K, fmt, like)
+    if out is None:
+        out = _new((M, N), torch.float32 if out_dtype is None else out_dtype, like, stream)
+    else:
+        _tensor(out, "out", like, (M, N))
+    dt = _out_dt(out)
+    e, preact = _epilogue(M, N, out, bias, act, want_preact, dropout_p, seed, step, residual, stream)
+    wsb = qfp4_gemm_epilogue_workspace_bytes(M, N, K, fmt)
+    if workspace is None and wsb:
+        workspace = _new((wsb,), torch.uint8, like, stream)
+    with _launch_on(like, stream) as s:
+        st = qfp4_gemm_epilogue(_ptr(A["codes"]), _ptr(A["scales"]), _ptr(A.get("tscale")), _ptr(B["codes"]),
+                                _ptr(B["scales"]), _ptr(B.get("tscale")), M, N, K, fmt, e, dt, _ptr(out),
+                                _ptr(workspace), workspace.nbytes if workspace is not None else 0, s)
+    _check(st, "qfp4_gemm_epilogue")
+    return out, preact
+
+
+def linear_forward_epilogue(X, W, fmt=NVFP4, four6=False, bias=None, act=ACT_NONE, want_preact=False, dropout_p=0.0,
+                            seed=0, step=None, residual=None, out_dtype=None, out=None, workspace=None, stream=None):
+    """``linear_forward`` with the epilogue of ``gemm_epilogue``
+    (qfp4_linear_forward_epilogue); returns (Y, preact)."""
+    torch = _torch()
+    _input(X, "X")
+    _input(W, "W")
+    M, K = X.shape
+    N = W.shape[0]
+    _tensor(X, "X", W, (M, W.shape[1]), torch.bfloat16)
+    _tensor(W, "W", X, dtype=torch.bfloat16)
+    if out is None:
+        out = _new((M, N), torch.float32 if out_dtype is None else out_dtype, X, stream)
+    else:
+        _tensor(out, "out", X, (M, N))
+    dt = _out_dt(out)
+    e, preact = _epilogue(M, N, out, bias, act, want_preact, dropout_p, seed, step, residual, stream)
+    wsb = qfp4_linear_forward_workspace_bytes(M, N, K, fmt)
+    if workspace is None and wsb:
+        workspace = _new((wsb,), torch.uint8, X, stream)
+    with _launch_on(X, stream) as s:
+        st = qfp4_linear_forward_epilogue(_ptr(X), _ptr(W), M, N, K, fmt, int(four6), e, dt, _ptr(out),
+                                          _ptr(workspace), workspace.nbytes if workspace is not None else 0, s)
+    _check(st, "qfp4_linear_forward_epilogue")
+    return out, preact
+
+
+def epilogue_backward(dY, Z=None, act=ACT_NONE, dropout_p=0.0, seed=0, step=None, want_dbias=True, out=None,
+                      workspace=None, stream=None):
+    """(dZ, dbias) of an epilogue's dropout, activation and bias
+    (qfp4_epilogue_backward): dY (M, N) and the forward's preact Z, bf16 or
+    fp32; dZ of their type, dbias (N,) fp32 or None.  ``out`` may supply a
+    dict with dZ and dbias."""
+    torch = _torch()
+    _input(dY, "dY")
+    M, N = dY.shape
+    dt = _xdt(dY)
+    if Z is not None:
+        _tensor(Z, "Z", dY, (M, N), dY.dtype)
+    o = dict(out) if out is not None else {}
+    if "dZ" not in o:
+        o["dZ"] = _new((M, N), dY.dtype, dY, stream)
+    if want_dbias and "dbias" not in o:
+        o["dbias"] = _new((N,), torch.float32, dY, stream)
+    _tensor(o["dZ"], "dZ", dY, (M, N), dY.dtype)
+    db = o.get("dbias")
+    wsb = 0
+    if db is not None:
+        _tensor(db, "dbias", dY, (N,), torch.float32)
+        wsb = qfp4_epilogue_backward_workspace_bytes(M, N)
+        if workspace is None and wsb:
+            workspace = _new((wsb,), torch.uint8, dY, stream)
+    with _launch_on(dY, stream) as s:
+        st = qfp4_epilogue_backward(_ptr(dY), _ptr(Z), dt, M, N, act, dropout_p, seed, _step(step, dY), _ptr(o["dZ"]),
+                                    _ptr(db), _ptr(workspace), workspace.nbytes if workspace is not None else 0, s)
+    _check(st, "qfp4_epilogue_backward")
+    return o["dZ"], db
+
+
+def dropout(x, p, seed=0, step=None, residual=None, out=None, stream=None):
+    """x / (1 - p) where the Philox word of an element lets it stay, else 0,
+    plus the residual (qfp4_dropout); x bf16 or fp32 of any shape.  The same
+    call on the output's gradient is the backward pass."""
+    _input(x, "x", dims=None)
+    dt = _xdt(x)
+    if residual is not None:
+        _tensor(residual, "residual", x, x.shape, x.dtype)
+    if out is None:
+        out = _new(x.shape, x.dtype, x, stream)
+    else:
+        _tensor(out, "out", x, x.shape, x.dtype)
+    with _launch_on(x, stream) as s:
+        st = qfp4_dropout(_ptr(x), dt, x.numel(), p, seed, _step(step, x), _ptr(residual), _ptr(out), s)
+    _check(st, "qfp4_dropout")
+    return out
+
+
+def _norm_params(x, D, gamma, beta):
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _tensor(t, name, x, (D,))
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise TypeError("gamma and beta must have one dtype")
+    return _param_dt(gamma if gamma is not None else beta, "gamma and beta")
+
+
+def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, want_stats=True, out=None, stream=None):
+    """(y, mean, rstd) of the rows of x (M, D), bf16 or fp32
+    (qfp4_layernorm_forward); gamma and beta (D,) bf16 or fp32, or None; mean
+    and rstd (M,) fp32, or None without ``want_stats``.  ``out`` may supply a
+    dict with y, mean and rstd."""
+    torch = _torch()
+    _input(x, "x")
+    M, D = x.shape
+    dt, wdt = _xdt(x), _norm_params(x, D, gamma, beta)
+    o = dict(out) if out is not None else {}
+    if "y" not in o:
+        o["y"] = _new((M, D), x.dtype, x, stream)
+    _tensor(o["y"], "y", x, (M, D), x.dtype)
+    for k in ("mean", "rstd"):
+        if k not in o and want_stats:
+            o[k] = _new((M,), torch.float32, x, stream)
+        if o.get(k) is not None:
+            _tensor(o[k], k, x, (M,), torch.float32)
+    with _launch_on(x, stream) as s:
+        st = qfp4_layernorm_forward(_ptr(x), dt, M, D, _ptr(gamma), _ptr(beta), wdt, eps, _ptr(o["y"]),
+                                    _ptr(o.get("mean")), _ptr(o.get("rstd")), s)
+    _check(st, "qfp4_layernorm_forward")
+    return o["y"], o.get("mean"), o.get("rstd")
+
+
+def layernorm_backward(dy, x, gamma, mean, rstd, want_dx=True, want_dw=True, out=None, workspace=None, stream=None):
+    """(dx, dgamma, dbeta) of ``layernorm_forward`` (qfp4_layernorm_backward);
+    dx of x's type, dgamma and dbeta (D,) fp32; None for what is not wanted.
+    ``out`` may supply a dict with dx, dgamma and dbeta."""
+    torch = _torch()
+    _input(x, "x")
+    M, D = x.shape
+    dt, wdt = _xdt(x), _norm_params(x, D, gamma, None)
+    _tensor(dy, "dy", x, (M, D), x.dtype)
+    _tensor(mean, "mean", x, (M,), torch.float32)
+    _tensor(rstd, "rstd", x, (M,), torch.float32)
+    o = dict(out) if out is not None else {}
+    if want_dx and "dx" not in o:
+        o["dx"] = _new((M, D), x.dtype, x, stream)
+    if o.get("dx") is not None:
+        _tensor(o["dx"], "dx", x, (M, D), x.dtype)
+    wsb = 0
+    for k in ("dgamma", "dbeta"):
+        if want_dw and k not in o:
+            o[k] = _new((D,), torch.float32, x, stream)
+        if o.get(k) is not None:
+            _tensor(o[k], k, x, (D,), torch.float32)
+            wsb = qfp4_layernorm_backward_workspace_bytes(M, D)
+    if workspace is None and wsb:
+        workspace = _new((wsb,), torch.uint8, x, stream)
+    with _launch_on(x, stream) as s:
+        st = qfp4_layernorm_backward(_ptr(dy), _ptr(x), dt, M, D, _ptr(gamma), wdt, _ptr(mean), _ptr(rstd),
+                                     _ptr(o.get("dx")), _ptr(o.get("dgamma")), _ptr(o.get("dbeta")), _ptr(workspace),
+                                     workspace.nbytes if workspace is not None else 0, s)
+    _check(st, "qfp4_layernorm_backward")
+    return o.get("dx"), o.get("dgamma"), o.get("dbeta")
 
 
 def kl_calibrate(x, bins=2048, levels=8, grid=0, stream=None, out=None):

@@ -19,8 +19,12 @@ int quantize_mxfp8(const void *x, qfp4_dtype xdt, int64_t M, int64_t K, qfp4_rou
                    uint8_t *codes, uint8_t *scales, uint8_t *codesT, uint8_t *scalesT, cudaStream_t stream);
 int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                      const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
-                     qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream);
+                     qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream,
+                     const EpParams *epi = nullptr);
 size_t gemm_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt);
+int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
+                  const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
+                  const EpParams &ep, qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream);
 int gemm_fused_rq(const void *A_bf16, int64_t M, int64_t K, int rotate, int four6, qfp4_fmt fmt,
                   const uint8_t *B_codes, const uint8_t *B_scales, const float *B_tscale, int64_t N, void *workspace,
                   qfp4_dtype out_dt, void *out, cudaStream_t stream, const float *amax_in, float *amax_out);
@@ -200,6 +204,59 @@ extern "C" int qfp4_gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_sc
     if (!workspace || workspace_bytes < gemm_workspace(M, N, K, fmt)) return QFP4_ERR_ARG;
     return gemm_blockscaled(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, out_dt, out,
                             workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// The host checks of a caller's epilogue, and its device form.
+static int epilogue_check(const qfp4_epilogue *e, EpParams *p)
+{
+    *p = EpParams{};
+    if (!e) return QFP4_OK;
+    if (e->act < QFP4_ACT_NONE || e->act > QFP4_ACT_SILU) return QFP4_ERR_ARG;
+    if (e->bias && e->bias_dt != QFP4_BF16 && e->bias_dt != QFP4_F32) return QFP4_ERR_ARG;
+    if (e->residual && e->residual_dt != QFP4_BF16 && e->residual_dt != QFP4_F32) return QFP4_ERR_ARG;
+    if (!dropout_ok(e->dropout_p)) return QFP4_ERR_ARG;
+    if (!ok_align(e->bias) || !ok_align(e->residual) || !ok_align(e->preact) || !step_aligned(e->step))
+        return QFP4_ERR_ALIGN;
+    p->bias = e->bias;
+    p->residual = e->residual;
+    p->preact = e->preact;
+    p->bias_f32 = e->bias_dt == QFP4_F32;
+    p->residual_f32 = e->residual_dt == QFP4_F32;
+    p->act = e->act;
+    p->drop = drop_params(e->dropout_p, e->seed, e->step);
+    return QFP4_OK;
+}
+
+extern "C" size_t qfp4_gemm_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)
+{
+    return gemm_workspace(M, N, K, fmt);
+}
+
+extern "C" int qfp4_gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale,
+                                  const uint8_t *B_codes, const uint8_t *B_scales, const float *B_tscale, int64_t M,
+                                  int64_t N, int64_t K, qfp4_fmt fmt, const qfp4_epilogue *epilogue,
+                                  qfp4_dtype out_dt, void *out, void *workspace, size_t workspace_bytes,
+                                  qfp4_stream_t stream)
+{
+    if (fmt != QFP4_MXFP4 && fmt != QFP4_NVFP4 && fmt != QFP4_MXFP8) return QFP4_ERR_ARG;
+    if (out_dt != QFP4_BF16 && out_dt != QFP4_F32) return QFP4_ERR_ARG;
+    int st = gemm_shape_check(M, N, K, out_dt);
+    if (st != QFP4_OK) return st;
+    const bool product = M * N > 0 && K > 0;
+    if (M * N > 0 && !out) return QFP4_ERR_ARG;
+    if (product && (!A_codes || !A_scales || !B_codes || !B_scales)) return QFP4_ERR_ARG;
+    if (product && fmt == QFP4_NVFP4 && (!A_tscale || !B_tscale)) return QFP4_ERR_ARG;
+    if (!ok_align(A_codes) || !ok_align(A_scales) || !ok_align(B_codes) || !ok_align(B_scales) || !ok_align(out) ||
+        !ok_align(workspace))
+        return QFP4_ERR_ALIGN;
+    EpParams ep;
+    st = epilogue_check(epilogue, &ep);
+    if (st != QFP4_OK) return st;
+    if (M * N == 0) return QFP4_OK;
+    if (product && qfp4_gemm_epilogue_workspace_bytes(M, N, K, fmt) > (workspace ? workspace_bytes : 0))
+        return QFP4_ERR_ARG;
+    return gemm_epilogue(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, ep, out_dt, out,
+                         workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t qfp4_gemm_fused_rq_workspace_bytes(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)

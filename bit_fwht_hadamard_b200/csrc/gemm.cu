@@ -22,8 +22,11 @@
 // by a small prepass into 512-byte chunks (128 rows x 4 scales: byte
 // (r%32)*16 + (r/32)*4 + j), which the main loops load with plain TMA or
 // bulk copies; the chunks live in the caller's workspace.
+#include <type_traits>
+
 #include "qfp4_common.cuh"
 #include "quantize1d.cuh"
+#include "epilogue.cuh"
 
 namespace qfp4 {
 
@@ -266,10 +269,48 @@ __global__ void __launch_bounds__(256) k_sf_chunks(SfJob ja, SfJob jb, int Kg, i
     }
 }
 
+// ------------------------------------------------------------------ epilogue of two columns
+// The last step of qfp4_gemm_epilogue on the accumulators (a0, a1) of row
+// `row`, columns col and col + 1 (col even): z = alpha a + bias, the optional
+// copy of z, the activation, dropout, the residual, one rounding to the
+// output type.
+template <int OUT>
+__device__ __forceinline__ void ep_store2(void *dst, int64_t i, float v0, float v1)
+{
+    if (OUT == QFP4_F32)
+        *reinterpret_cast<float2 *>(static_cast<float *>(dst) + i) = make_float2(v0, v1);
+    else
+        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(dst) + i) = pack_bf16(v0, v1);
+}
+
+template <int OUT>
+__device__ __forceinline__ void ep_apply2(const EpParams &ep, void *out, int N, int row, int col, float alpha,
+                                          uint64_t step, float a0, float a1)
+{
+    const int64_t i = static_cast<int64_t>(row) * N + col;
+    float2 b = make_float2(0.0f, 0.0f);
+    if (ep.bias) b = ld2_as_float(ep.bias, ep.bias_f32, col);
+    const float z0 = fmaf(a0, alpha, b.x), z1 = fmaf(a1, alpha, b.y);
+    if (ep.preact) ep_store2<OUT>(ep.preact, i, z0, z1);
+    float y0 = act_forward(z0, ep.act), y1 = act_forward(z1, ep.act);
+    if (ep.drop.on) {
+        const uint4 w = drop_words4(ep.drop, step, static_cast<uint64_t>(i) >> 2);   // N % 4 == 0
+        y0 = drop1(ep.drop, y0, (i & 2) ? w.z : w.x);
+        y1 = drop1(ep.drop, y1, (i & 2) ? w.w : w.y);
+    }
+    if (ep.residual) {
+        const float2 r = ld2_as_float(ep.residual, ep.residual_f32, i);
+        y0 += r.x;
+        y1 += r.y;
+    }
+    ep_store2<OUT>(out, i, y0, y1);
+}
+
 // ------------------------------------------------------------------ main kernel
-template <int FMT, int OUT>
+template <int FMT, int OUT, bool EP>
 __global__ void __launch_bounds__(GM_THREADS, 1)
-    k_gemm_blockscaled(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p)
+    k_gemm_blockscaled(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p,
+                       EpParams ep)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -393,6 +434,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         const int h = (warp - 2) >> 2;            // column half
         float alpha = 1.0f;
         if (FMT == QFP4_NVFP4) alpha = __fmul_rn(*p.tA, *p.tB);
+        const uint64_t step = EP ? drop_step(ep.drop) : 0ull;
         int ti = 0;
         for (int t = blockIdx.x; t < ntiles && !abort_flag; t += gridDim.x, ++ti) {
             int mb, nb;
@@ -420,7 +462,14 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int row = mb * GM_BM + 32 * q + 16 * hh + 8 * e + (lane >> 2);
                     if (row >= p.M) continue;
-                    if (OUT == QFP4_F32) {
+                    if constexpr (EP) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (col0 + 8 * j < p.N)
+                                ep_apply2<OUT>(ep, p.out, p.N, row, col0 + 8 * j, alpha, step,
+                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e]),
+                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e + 1]));
+                    } else if (OUT == QFP4_F32) {
                         float *o = static_cast<float *>(p.out) + static_cast<int64_t>(row) * p.N + col0;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -611,10 +660,11 @@ __device__ __forceinline__ void g2_exit(uint32_t tmem, bool dealloc)
     if (dealloc) tmem_dealloc_cg2(tmem, GM_TMEM_COLS);
 }
 
-template <int FMT, int OUT>
+template <int FMT, int OUT, bool EP>
 __global__ void __launch_bounds__(G2_THREADS, 1)
     k_gemm_bs2(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, GemmParams p)
+               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, GemmParams p,
+               EpParams ep)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -840,6 +890,7 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
         const uint32_t acc_empty_leader = mapa_shared(smem_u32(&acc_empty), 0);
         float alpha = 1.0f;
         if (FMT == QFP4_NVFP4) alpha = __fmul_rn(*p.tA, *p.tB);
+        const uint64_t step = EP ? drop_step(ep.drop) : 0ull;
         int ti = 0;
         for (int t = cluster; t < ntiles && !abort_flag; t += nclusters, ++ti) {
             int mb, nb;
@@ -866,7 +917,14 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int row = row_base + 32 * q + 16 * hh + 8 * e + (lane >> 2);
                     if (row >= p.M) continue;
-                    if (OUT == QFP4_F32) {
+                    if constexpr (EP) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (col0 + 8 * j < p.N)
+                                ep_apply2<OUT>(ep, p.out, p.N, row, col0 + 8 * j, alpha, step,
+                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e]),
+                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e + 1]));
+                    } else if (OUT == QFP4_F32) {
                         float *o = static_cast<float *>(p.out) + static_cast<int64_t>(row) * p.N + col0;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -932,12 +990,13 @@ int rearrange_scales(const uint8_t *a_scales, int64_t M, int n_blocks_a, uint8_t
     return QFP4_OK;
 }
 
-template <int FMT, int OUT>
-static int launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const GemmParams &p, int grid, cudaStream_t s)
+template <int FMT, int OUT, bool EP>
+static int launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const GemmParams &p, const EpParams &ep, int grid,
+                       cudaStream_t s)
 {
-    auto kern = k_gemm_blockscaled<FMT, OUT>;
-    if (ensure_dyn_smem<k_gemm_blockscaled<FMT, OUT>>(GM_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
-    if (launch_pdl(kern, dim3(grid), dim3(GM_THREADS), GM_SMEM, s, ta, tb, p) != cudaSuccess) {
+    auto kern = k_gemm_blockscaled<FMT, OUT, EP>;
+    if (ensure_dyn_smem<k_gemm_blockscaled<FMT, OUT, EP>>(GM_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
+    if (launch_pdl(kern, dim3(grid), dim3(GM_THREADS), GM_SMEM, s, ta, tb, p, ep) != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
@@ -945,12 +1004,12 @@ static int launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const GemmP
     return QFP4_OK;
 }
 
-template <int FMT, int OUT>
+template <int FMT, int OUT, bool EP>
 static int launch_gemm2(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tsa, const CUtensorMap &tsb,
-                        const GemmParams &p, int grid, cudaStream_t s)
+                        const GemmParams &p, const EpParams &ep, int grid, cudaStream_t s)
 {
-    auto kern = k_gemm_bs2<FMT, OUT>;
-    if (ensure_dyn_smem<k_gemm_bs2<FMT, OUT>>(G2_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
+    auto kern = k_gemm_bs2<FMT, OUT, EP>;
+    if (ensure_dyn_smem<k_gemm_bs2<FMT, OUT, EP>>(G2_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(G2_THREADS, 1, 1);
@@ -965,7 +1024,7 @@ static int launch_gemm2(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, p, ep) != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
@@ -973,12 +1032,32 @@ static int launch_gemm2(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
     return QFP4_OK;
 }
 
+// Calls launch(format, output type, epilogue or not) with the three as
+// compile-time constants.
+template <typename F>
+static int dispatch_gemm(qfp4_fmt fmt, qfp4_dtype out_dt, const EpParams *epi, F launch)
+{
+    auto by_ep = [&](auto f, auto o) {
+        return epi ? launch(f, o, std::integral_constant<bool, true>{})
+                   : launch(f, o, std::integral_constant<bool, false>{});
+    };
+    auto by_out = [&](auto f) {
+        return out_dt == QFP4_F32 ? by_ep(f, std::integral_constant<int, QFP4_F32>{})
+                                  : by_ep(f, std::integral_constant<int, QFP4_BF16>{});
+    };
+    if (fmt == QFP4_MXFP8) return by_out(std::integral_constant<int, QFP4_MXFP8>{});
+    if (fmt == QFP4_NVFP4) return by_out(std::integral_constant<int, QFP4_NVFP4>{});
+    return by_out(std::integral_constant<int, QFP4_MXFP4>{});
+}
+
 // Main kernel on already rearranged scales (sfa / sfb in the chunk layout).
 // Problems taller than one 128-row block run on CTA pairs (256 x 256 tiles),
-// the rest on single CTAs (128 x 256 tiles).
+// the rest on single CTAs (128 x 256 tiles).  epi: the epilogue's options,
+// or NULL for the plain product.
 int gemm_core(const uint8_t *A_codes, const uint8_t *sfa, const float *A_tscale, const uint8_t *B_codes,
               const uint8_t *sfb, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
-              qfp4_dtype out_dt, void *out, cudaStream_t stream)
+              qfp4_dtype out_dt, void *out, cudaStream_t stream,
+              const EpParams *epi = nullptr)
 {
     const GemmLayout L = gemm_layout(M, N, K, fmt);
     const bool pair = M > GM_BM;
@@ -1036,36 +1115,57 @@ int gemm_core(const uint8_t *A_codes, const uint8_t *sfa, const float *A_tscale,
         }
         const int ntiles = static_cast<int>(((M + G2_BM - 1) / G2_BM) * ((N + G2_BN - 1) / G2_BN));
         const int grid = 2 * imin<int>(ntiles, num_sms() / 2);
-        if (fmt == QFP4_MXFP8)
-            return out_dt == QFP4_F32 ? launch_gemm2<QFP4_MXFP8, QFP4_F32>(ta, tb, tsa, tsb, p, grid, stream)
-                                      : launch_gemm2<QFP4_MXFP8, QFP4_BF16>(ta, tb, tsa, tsb, p, grid, stream);
-        if (fmt == QFP4_NVFP4)
-            return out_dt == QFP4_F32 ? launch_gemm2<QFP4_NVFP4, QFP4_F32>(ta, tb, tsa, tsb, p, grid, stream)
-                                      : launch_gemm2<QFP4_NVFP4, QFP4_BF16>(ta, tb, tsa, tsb, p, grid, stream);
-        return out_dt == QFP4_F32 ? launch_gemm2<QFP4_MXFP4, QFP4_F32>(ta, tb, tsa, tsb, p, grid, stream)
-                                  : launch_gemm2<QFP4_MXFP4, QFP4_BF16>(ta, tb, tsa, tsb, p, grid, stream);
+        return dispatch_gemm(fmt, out_dt, epi, [&](auto f, auto o, auto e) {
+            return launch_gemm2<f.value, o.value, e.value>(ta, tb, tsa, tsb, p, epi ? *epi : EpParams{}, grid, stream);
+        });
     }
     const int grid = static_cast<int>(imin<int64_t>(static_cast<int64_t>(L.MB) * L.NT, num_sms()));
-    if (fmt == QFP4_MXFP8)
-        return out_dt == QFP4_F32 ? launch_gemm<QFP4_MXFP8, QFP4_F32>(ta, tb, p, grid, stream)
-                                  : launch_gemm<QFP4_MXFP8, QFP4_BF16>(ta, tb, p, grid, stream);
-    if (fmt == QFP4_NVFP4)
-        return out_dt == QFP4_F32 ? launch_gemm<QFP4_NVFP4, QFP4_F32>(ta, tb, p, grid, stream)
-                                  : launch_gemm<QFP4_NVFP4, QFP4_BF16>(ta, tb, p, grid, stream);
-    return out_dt == QFP4_F32 ? launch_gemm<QFP4_MXFP4, QFP4_F32>(ta, tb, p, grid, stream)
-                              : launch_gemm<QFP4_MXFP4, QFP4_BF16>(ta, tb, p, grid, stream);
+    return dispatch_gemm(fmt, out_dt, epi, [&](auto f, auto o, auto e) {
+        return launch_gemm<f.value, o.value, e.value>(ta, tb, p, epi ? *epi : EpParams{}, grid, stream);
+    });
 }
 
 int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                      const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
-                     qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream)
+                     qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream, const EpParams *epi)
 {
     const GemmLayout L = gemm_layout(M, N, K, fmt);
     uint8_t *sfa = static_cast<uint8_t *>(workspace);
     uint8_t *sfb = sfa + L.sfa_bytes;
     const int st = rearrange_scales(A_scales, M, L.MB, sfa, B_scales, N, 2 * L.NT, sfb, K, fmt, L.NC, stream);
     if (st != QFP4_OK) return st;
-    return gemm_core(A_codes, sfa, A_tscale, B_codes, sfb, B_tscale, M, N, K, fmt, out_dt, out, stream);
+    return gemm_core(A_codes, sfa, A_tscale, B_codes, sfb, B_tscale, M, N, K, fmt, out_dt, out, stream, epi);
+}
+
+// ------------------------------------------------------------------ GEMM with an epilogue
+// K == 0: every sum is zero, the epilogue alone remains.
+template <int OUT>
+__global__ void __launch_bounds__(256) k_epilogue_of_zero(EpParams ep, void *out, int M, int N)
+{
+    const uint64_t step = drop_step(ep.drop);
+    const int64_t pairs = static_cast<int64_t>(M) * (N / 2);
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < pairs;
+         t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int row = static_cast<int>(t / (N / 2)), col = 2 * static_cast<int>(t % (N / 2));
+        ep_apply2<OUT>(ep, out, N, row, col, 1.0f, step, 0.0f, 0.0f);
+    }
+}
+
+int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
+                  const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
+                  const EpParams &ep, qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream)
+{
+    if (K == 0) {
+        const int grid = static_cast<int>(imin<int64_t>((M * (N / 2) + 255) / 256, 8 * num_sms()));
+        if (out_dt == QFP4_F32)
+            k_epilogue_of_zero<QFP4_F32><<<grid, 256, 0, stream>>>(ep, out, static_cast<int>(M), static_cast<int>(N));
+        else
+            k_epilogue_of_zero<QFP4_BF16><<<grid, 256, 0, stream>>>(ep, out, static_cast<int>(M), static_cast<int>(N));
+        QFP4_LAUNCH_CHECK();
+        return QFP4_OK;
+    }
+    return gemm_blockscaled(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, out_dt, out,
+                            workspace, stream, &ep);
 }
 
 // ------------------------------------------------------------------ fused rotate + quantize + GEMM

@@ -9,3 +9,5 @@
 #include "gemm_noalloc.cu"
 #include "linear.cu"
 #include "calib.cu"
+#include "dropout.cu"
+#include "layernorm.cu"

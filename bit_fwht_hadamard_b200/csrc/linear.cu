@@ -24,7 +24,8 @@ int quantize_mxfp8_columns(const void *x, qfp4_dtype xdt, int64_t M, int64_t K, 
                            uint8_t *codesT, uint8_t *scalesT, cudaStream_t stream);
 int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                      const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
-                     qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream);
+                     qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream,
+                     const EpParams *epi);
 size_t gemm_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt);
 
 // Bump allocator over the caller's workspace (256-byte aligned pieces).
@@ -153,19 +154,22 @@ extern "C" size_t qfp4_linear_forward_workspace_bytes(int64_t M, int64_t N, int6
     return linear_fwd_layout(M, N, K, fmt, nullptr, nullptr, nullptr, nullptr, nullptr);
 }
 
-extern "C" int qfp4_linear_forward(const void *X, const void *W, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
-                                   int four6, qfp4_dtype out_dt, void *Y, void *workspace, size_t workspace_bytes,
-                                   qfp4_stream_t stream_)
+static int linear_forward(const void *X, const void *W, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt, int four6,
+                          const EpParams *ep, qfp4_dtype out_dt, void *Y, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream)
 {
-    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int st = linear_fwd_check(M, N, K, fmt, four6, out_dt);
     if (st != QFP4_OK) return st;
     if (M * N > 0 && (!X || !W || !Y)) return QFP4_ERR_ARG;
     if (!aligned16(X) || !aligned16(W) || !aligned16(Y) || !aligned16(workspace)) return QFP4_ERR_ALIGN;
     if (M * N == 0) return QFP4_OK;
-    if (K == 0)
+    if (K == 0) {
+        if (ep)
+            return gemm_epilogue(nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, M, N, 0, fmt, *ep, out_dt, Y,
+                                 nullptr, stream);
         return cudaMemsetAsync(Y, 0, M * N * (out_dt == QFP4_F32 ? 4 : 2), stream) == cudaSuccess ? QFP4_OK
                                                                                                    : QFP4_ERR_CUDA;
+    }
     if (!workspace || workspace_bytes < qfp4_linear_forward_workspace_bytes(M, N, K, fmt)) return QFP4_ERR_ARG;
     Operand xq, wq;
     float *partials;
@@ -177,8 +181,31 @@ extern "C" int qfp4_linear_forward(const void *X, const void *W, int64_t M, int6
     s = quantize1d(W, QFP4_BF16, N * K, fmt, QFP4_RNE, 1, four6, 0, wq.codes, wq.scales, wq.tscale, partials, nullptr,
                    stream);
     if (s != QFP4_OK) return s;
+    if (ep)
+        return gemm_epilogue(xq.codes, xq.scales, xq.tscale, wq.codes, wq.scales, wq.tscale, M, N, K, fmt, *ep, out_dt,
+                             Y, gws, stream);
     return gemm_blockscaled(xq.codes, xq.scales, xq.tscale, wq.codes, wq.scales, wq.tscale, M, N, K, fmt, out_dt, Y,
                             gws, stream);
+}
+
+extern "C" int qfp4_linear_forward(const void *X, const void *W, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
+                                   int four6, qfp4_dtype out_dt, void *Y, void *workspace, size_t workspace_bytes,
+                                   qfp4_stream_t stream)
+{
+    return linear_forward(X, W, M, N, K, fmt, four6, nullptr, out_dt, Y, workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int qfp4_linear_forward_epilogue(const void *X, const void *W, int64_t M, int64_t N, int64_t K,
+                                            qfp4_fmt fmt, int four6, const qfp4_epilogue *epilogue,
+                                            qfp4_dtype out_dt, void *Y, void *workspace, size_t workspace_bytes,
+                                            qfp4_stream_t stream)
+{
+    EpParams ep;
+    const int st = epilogue_check(epilogue, &ep);
+    if (st != QFP4_OK) return st;
+    return linear_forward(X, W, M, N, K, fmt, four6, &ep, out_dt, Y, workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t qfp4_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)

@@ -96,6 +96,6 @@ extern "C" int qfp4_selftest_wait_timeout(int64_t limit_us, qfp4_stream_t stream
     return QFP4_OK;
 }
 
-extern "C" int qfp4_version(void) { return 200; }
+extern "C" int qfp4_version(void) { return 300; }
 
 extern "C" uint64_t qfp4_launch_count(void) { return qfp4::g_launches.load(std::memory_order_relaxed); }

@@ -70,6 +70,15 @@ typedef enum {
     QFP4_SCALE_E4M3_UP = 2      /* NVFP4 only: E4M3 block scale rounded up (no element clips) */
 } qfp4_scale_rule;
 
+/* Activations of an epilogue (see qfp4_epilogue). */
+typedef enum {
+    QFP4_ACT_NONE = 0,
+    QFP4_ACT_RELU = 1,          /* max(z, 0)                                                 */
+    QFP4_ACT_GELU = 2,          /* z Phi(z), Phi the normal distribution function            */
+    QFP4_ACT_GELU_TANH = 3,     /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))             */
+    QFP4_ACT_SILU = 4           /* z / (1 + e^-z)                                            */
+} qfp4_act;
+
 enum {
     QFP4_OK = 0,
     QFP4_ERR_ARG = -1,          /* NULL where a buffer is required, bad enum, short workspace */
@@ -363,6 +372,137 @@ size_t qfp4_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, qfp
 int qfp4_linear_backward(const void *G, const void *X, const void *W, int64_t M, int64_t N, int64_t K,
                          qfp4_fmt fmt, uint64_t seed, qfp4_dtype out_dt, void *dX, void *dW,
                          void *workspace, size_t workspace_bytes, qfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qfp4_epilogue -- what a GEMM or linear call does with each sum before it
+ * stores it, instead of separate passes over the M x N output:
+ *   z = sum + bias[n];  v = act(z);  v = dropout(v);  y = v + residual[m][n]
+ * in binary32, rounded once to the output type.  No counterpart on the source
+ * pages: they are the steps a transformer puts right after its linear layers.
+ * Zero-initialise the struct; a zero or NULL field leaves its step out.
+ *   bias       N values of type bias_dt, or NULL.
+ *   act        a qfp4_act.
+ *   preact     out, M x N of the call's output type, or NULL: z, as
+ *              qfp4_epilogue_backward needs it.  Must not overlap out.
+ *   dropout_p, seed, step   as in qfp4_dropout, with e = m*N + n; 0 <= p < 1.
+ *   residual   M x N of type residual_dt, or NULL.  May be the out buffer
+ *              itself where residual_dt is the output type.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    const void *bias;
+    const void *residual;
+    void *preact;
+    const uint64_t *step;
+    uint64_t seed;
+    double dropout_p;
+    qfp4_dtype bias_dt;
+    qfp4_dtype residual_dt;
+    qfp4_act act;
+} qfp4_epilogue;
+
+/* ------------------------------------------------------------------------
+ * qfp4_gemm_epilogue -- qfp4_gemm_blockscaled followed by an epilogue, in one
+ * kernel: out = epilogue(deq(A) deq(B)^T).  Operands, shape rules and errors
+ * as there; K == 0 gives the epilogue of zero sums.  epilogue: host memory,
+ * read before the call returns; NULL for none.
+ * workspace: at least qfp4_gemm_epilogue_workspace_bytes(M, N, K, fmt) bytes
+ *   of device scratch (NULL where that is 0); contents on entry do not matter.
+ * The sums' order over K may differ from qfp4_gemm_blockscaled's; results are
+ * the same for the same arguments.
+ * Errors: as qfp4_gemm_blockscaled; QFP4_ERR_ARG for an unknown act or type,
+ *   dropout_p outside [0, 1); QFP4_ERR_ALIGN for a bias, residual or preact
+ *   off 16 bytes, or a step off 8.
+ * ---------------------------------------------------------------------- */
+size_t qfp4_gemm_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt);
+
+int qfp4_gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale,
+                       const uint8_t *B_codes, const uint8_t *B_scales, const float *B_tscale,
+                       int64_t M, int64_t N, int64_t K, qfp4_fmt fmt, const qfp4_epilogue *epilogue,
+                       qfp4_dtype out_dt, void *out, void *workspace, size_t workspace_bytes,
+                       qfp4_stream_t stream);
+
+/* qfp4_linear_forward with an epilogue: Y = epilogue(Q(X H) Q(W H)^T).
+ * workspace: qfp4_linear_forward_workspace_bytes(M, N, K, fmt) bytes. */
+int qfp4_linear_forward_epilogue(const void *X, const void *W, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
+                                 int four6, const qfp4_epilogue *epilogue, qfp4_dtype out_dt, void *Y,
+                                 void *workspace, size_t workspace_bytes, qfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qfp4_epilogue_backward -- the backward pass of an epilogue's dropout,
+ * activation and bias: dZ = dropout(dY) * act'(Z), dbias = the column sums of
+ * dZ (before its rounding).  The residual's gradient is dY itself; dZ is the
+ * G that qfp4_linear_backward takes.
+ *   dY, Z, dZ  M x N of type dt (any M and N); Z the forward's preact (NULL
+ *              with QFP4_ACT_NONE).  dZ may be dY or Z itself.
+ *   act, dropout_p, seed, step   the forward's (step: the value it had then).
+ *   dbias      N binary32 sums, or NULL.
+ *   workspace  with dbias: qfp4_epilogue_backward_workspace_bytes(M, N) bytes
+ *              of device scratch, else may be NULL.
+ * The sums' order is fixed: the same arguments give the same bits.
+ * Errors: QFP4_ERR_ARG for a bad enum, dropout_p outside [0, 1), a missing
+ *   buffer or a short workspace; QFP4_ERR_SHAPE for M or N negative or 2^30
+ *   and above; QFP4_ERR_ALIGN as in qfp4_gemm_epilogue.
+ * ---------------------------------------------------------------------- */
+size_t qfp4_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
+
+int qfp4_epilogue_backward(const void *dY, const void *Z, qfp4_dtype dt, int64_t M, int64_t N, qfp4_act act,
+                           double dropout_p, uint64_t seed, const uint64_t *step, void *dZ, float *dbias,
+                           void *workspace, size_t workspace_bytes, qfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qfp4_dropout -- out[e] = (e stays ? x[e] / (1 - p) : 0) + residual[e], for
+ * e = 0 .. n - 1, in binary32, rounded once to dt.  e stays iff word e mod 4
+ * of Philox4x32-10 keyed (seed low 32, seed high 32) at counter (e/4 low 32,
+ * e/4 high 32, step low 32, step high 32 + 2^31) is >= floor(p 2^32).  The
+ * mask is never stored: the same call on the output's gradient (with no
+ * residual) is the backward pass.  The counters are not those of the
+ * stochastic rounding, so one seed may serve both.
+ *   p      0 <= p < 1; p == 0 keeps everything.
+ *   step   device pointer to a counter below 2^63 (8-byte aligned), read when
+ *          the kernel runs, so that each replay of a captured graph can draw
+ *          a mask of its own; NULL for 0.
+ *   residual   n values of type dt, or NULL.
+ *   out    n values of type dt; may be x or residual itself.
+ * Errors: QFP4_ERR_ARG for p outside [0, 1), a bad type or a missing buffer;
+ *   QFP4_ERR_SHAPE for n < 0 or n > 2^38; QFP4_ERR_ALIGN.
+ * ---------------------------------------------------------------------- */
+int qfp4_dropout(const void *x, qfp4_dtype dt, int64_t n, double p, uint64_t seed, const uint64_t *step,
+                 const void *residual, void *out, qfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qfp4_layernorm_forward -- y = (x - mean) rstd gamma + beta over each row of
+ * an M x D matrix, rstd = 1 / sqrt(var + eps), var the mean of (x - mean)^2;
+ * statistics in binary32, y rounded once.
+ *   x, y         M x D of type dt, any M and any D >= 1.  y may be x itself.
+ *   gamma, beta  D values of type wdt; NULL for ones / zeros.
+ *   eps          >= 0.
+ *   mean, rstd   out, M binary32 values each, or NULL (not kept).
+ * Errors: QFP4_ERR_ARG, QFP4_ERR_ALIGN; QFP4_ERR_SHAPE for D == 0 with rows,
+ *   M or D negative or 2^30 and above, or more than 2^38 elements.
+ * ---------------------------------------------------------------------- */
+int qfp4_layernorm_forward(const void *x, qfp4_dtype dt, int64_t M, int64_t D, const void *gamma, const void *beta,
+                           qfp4_dtype wdt, float eps, void *y, float *mean, float *rstd, qfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * qfp4_layernorm_backward -- with xhat = (x - mean) rstd and g = dy gamma:
+ * dx = rstd (g - mean_d(g) - xhat mean_d(g xhat)), dgamma = the column sums
+ * of dy xhat, dbeta = the column sums of dy (binary32, in a fixed order: the
+ * same arguments give the same bits).
+ *   dy, x, dx      M x D of type dt; dx may be dy itself.
+ *   gamma          D values of type wdt; NULL for ones.
+ *   mean, rstd     the forward's.
+ *   dgamma, dbeta  out, D binary32 values each.
+ *   dx, dgamma, dbeta   any of them may be NULL (not computed), not all.
+ *   workspace      with dgamma or dbeta:
+ *                  qfp4_layernorm_backward_workspace_bytes(M, D) bytes of
+ *                  device scratch, else may be NULL.
+ * Errors: as the forward's; QFP4_ERR_ARG for a short workspace.
+ * ---------------------------------------------------------------------- */
+size_t qfp4_layernorm_backward_workspace_bytes(int64_t M, int64_t D);
+
+int qfp4_layernorm_backward(const void *dy, const void *x, qfp4_dtype dt, int64_t M, int64_t D, const void *gamma,
+                            qfp4_dtype wdt, const float *mean, const float *rstd, void *dx, float *dgamma,
+                            float *dbeta, void *workspace, size_t workspace_bytes, qfp4_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * qfp4_kl_calibrate -- KL-divergence clip point of an activation tensor
