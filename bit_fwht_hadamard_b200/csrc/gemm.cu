@@ -269,43 +269,6 @@ __global__ void __launch_bounds__(256) k_sf_chunks(SfJob ja, SfJob jb, int Kg, i
     }
 }
 
-// ------------------------------------------------------------------ epilogue of two columns
-// The last step of qfp4_gemm_epilogue on the accumulators (a0, a1) of row
-// `row`, columns col and col + 1 (col even): z = alpha a + bias, the optional
-// copy of z, the activation, dropout, the residual, one rounding to the
-// output type.
-template <int OUT>
-__device__ __forceinline__ void ep_store2(void *dst, int64_t i, float v0, float v1)
-{
-    if (OUT == QFP4_F32)
-        *reinterpret_cast<float2 *>(static_cast<float *>(dst) + i) = make_float2(v0, v1);
-    else
-        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(dst) + i) = pack_bf16(v0, v1);
-}
-
-template <int OUT>
-__device__ __forceinline__ void ep_apply2(const EpParams &ep, void *out, int N, int row, int col, float alpha,
-                                          uint64_t step, float a0, float a1)
-{
-    const int64_t i = static_cast<int64_t>(row) * N + col;
-    float2 b = make_float2(0.0f, 0.0f);
-    if (ep.bias) b = ld2_as_float(ep.bias, ep.bias_f32, col);
-    const float z0 = fmaf(a0, alpha, b.x), z1 = fmaf(a1, alpha, b.y);
-    if (ep.preact) ep_store2<OUT>(ep.preact, i, z0, z1);
-    float y0 = act_forward(z0, ep.act), y1 = act_forward(z1, ep.act);
-    if (ep.drop.on) {
-        const uint4 w = drop_words4(ep.drop, step, static_cast<uint64_t>(i) >> 2);   // N % 4 == 0
-        y0 = drop1(ep.drop, y0, (i & 2) ? w.z : w.x);
-        y1 = drop1(ep.drop, y1, (i & 2) ? w.w : w.y);
-    }
-    if (ep.residual) {
-        const float2 r = ld2_as_float(ep.residual, ep.residual_f32, i);
-        y0 += r.x;
-        y1 += r.y;
-    }
-    ep_store2<OUT>(out, i, y0, y1);
-}
-
 // ------------------------------------------------------------------ main kernel
 template <int FMT, int OUT, bool EP>
 __global__ void __launch_bounds__(GM_THREADS, 1)
@@ -441,11 +404,18 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             tile_coords(t, p.tiles_m, p.tiles_n, mb, nb);
             if (!warp_wait(&acc_full, ti & 1)) { abort_flag = 1; break; }
             tc_fence_after();
-            // two 16-lane halves of this warp's quadrant, 128 columns each
             uint32_t r[128];
+            if constexpr (EP) {
+                // a lane a row: 128 columns of its own
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-                tmem_ld16x256b_x16(tmem + (static_cast<uint32_t>(32 * q + 16 * hh) << 16) + 128 * h, r + 64 * hh);
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * h + 32 * c, r + 32 * c);
+            } else {
+                // two 16-lane halves of this warp's quadrant, 128 columns each
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tmem_ld16x256b_x16(tmem + (static_cast<uint32_t>(32 * q + 16 * hh) << 16) + 128 * h, r + 64 * hh);
+            }
             tmem_ld_wait();
             reg_fence<128>(r);
             // the accumulator is in registers: hand it back before the stores
@@ -453,6 +423,11 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty);
 
+            if constexpr (EP) {
+                const int row = mb * GM_BM + 32 * q + lane;
+                if (row < p.M) ep_row128<OUT>(ep, p.out, p.N, row, nb * GM_BN + 128 * h, alpha, step, r);
+                continue;
+            }
             // r[64hh + 4j + {0,1}]: row 32q + 16hh + lane/4, columns 8j + 2(lane%4) + {0,1};
             // r[64hh + 4j + {2,3}]: the row 8 below.  Four lanes cover 32 contiguous bytes.
             const int col0 = nb * GM_BN + 128 * h + 2 * (lane & 3);
@@ -462,14 +437,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int row = mb * GM_BM + 32 * q + 16 * hh + 8 * e + (lane >> 2);
                     if (row >= p.M) continue;
-                    if constexpr (EP) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (col0 + 8 * j < p.N)
-                                ep_apply2<OUT>(ep, p.out, p.N, row, col0 + 8 * j, alpha, step,
-                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e]),
-                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e + 1]));
-                    } else if (OUT == QFP4_F32) {
+                    if (OUT == QFP4_F32) {
                         float *o = static_cast<float *>(p.out) + static_cast<int64_t>(row) * p.N + col0;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -895,12 +863,24 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
         for (int t = cluster; t < ntiles && !abort_flag; t += nclusters, ++ti) {
             int mb, nb;
             tile_coords(t, tiles_m, tiles_n, mb, nb);
+            if constexpr (EP) {
+                const int row = mb * G2_BM + 128 * static_cast<int>(rank) + 32 * q + lane;
+                if (ep.residual && row < p.M) ep_prefetch128(ep, p.N, row, nb * G2_BN + 128 * h);
+            }
             if (!warp_wait(&acc_full, ti & 1)) { abort_flag = 1; break; }
             tc_fence_after();
             uint32_t r[128];
+            if constexpr (EP) {
+                // a lane a row: 128 columns of its own
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-                tmem_ld16x256b_x16(tmem + (static_cast<uint32_t>(32 * q + 16 * hh) << 16) + 128 * h, r + 64 * hh);
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * h + 32 * c, r + 32 * c);
+            } else {
+                // two 16-lane halves of this warp's quadrant, 128 columns each
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    tmem_ld16x256b_x16(tmem + (static_cast<uint32_t>(32 * q + 16 * hh) << 16) + 128 * h, r + 64 * hh);
+            }
             tmem_ld_wait();
             reg_fence<128>(r);
             // the accumulator is in registers: hand it back at once, so the
@@ -909,22 +889,20 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
 
-            const int col0 = nb * G2_BN + 128 * h + 2 * (lane & 3);
             const int row_base = mb * G2_BM + 128 * static_cast<int>(rank);
+            if constexpr (EP) {
+                const int row = row_base + 32 * q + lane;
+                if (row < p.M) ep_row128<OUT>(ep, p.out, p.N, row, nb * G2_BN + 128 * h, alpha, step, r);
+                continue;
+            }
+            const int col0 = nb * G2_BN + 128 * h + 2 * (lane & 3);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = row_base + 32 * q + 16 * hh + 8 * e + (lane >> 2);
                     if (row >= p.M) continue;
-                    if constexpr (EP) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (col0 + 8 * j < p.N)
-                                ep_apply2<OUT>(ep, p.out, p.N, row, col0 + 8 * j, alpha, step,
-                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e]),
-                                               __uint_as_float(r[64 * hh + 4 * j + 2 * e + 1]));
-                    } else if (OUT == QFP4_F32) {
+                    if (OUT == QFP4_F32) {
                         float *o = static_cast<float *>(p.out) + static_cast<int64_t>(row) * p.N + col0;
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
@@ -1138,29 +1116,40 @@ int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const floa
 }
 
 // ------------------------------------------------------------------ GEMM with an epilogue
-// K == 0: every sum is zero, the epilogue alone remains.
+// K == 0: every sum is zero, the epilogue alone remains.  A thread takes
+// sixteen columns of a row.
 template <int OUT>
-__global__ void __launch_bounds__(256) k_epilogue_of_zero(EpParams ep, void *out, int M, int N)
+__global__ void __launch_bounds__(128) k_epilogue_of_zero(EpParams ep, void *out, int M, int N)
 {
     const uint64_t step = drop_step(ep.drop);
-    const int64_t pairs = static_cast<int64_t>(M) * (N / 2);
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < pairs;
+    const int per_row = (N + 15) / 16;
+    const int64_t chunks = static_cast<int64_t>(M) * per_row;
+    const uint32_t zero[16] = {};
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < chunks;
          t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int row = static_cast<int>(t / (N / 2)), col = 2 * static_cast<int>(t % (N / 2));
-        ep_apply2<OUT>(ep, out, N, row, col, 1.0f, step, 0.0f, 0.0f);
+        const int64_t row = t / per_row;
+        const int col = 16 * static_cast<int>(t % per_row), nc = imin(16, N - col);
+        ep_chunk16<OUT>(ep, out, row * N + col, col, nc, 1.0f, step, zero);
     }
 }
 
 int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                   const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
-                  const EpParams &ep, qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream)
+                  const EpParams &epi, qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream)
 {
+    EpParams ep = epi;
+    // 32-byte accesses where each row of every M x N buffer starts on 32 bytes
+    auto rows32 = [&](const void *p, int f32) {
+        return !p || ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(N * (f32 ? 4 : 2))) & 31u) == 0;
+    };
+    ep.wide = rows32(out, out_dt == QFP4_F32) && rows32(ep.preact, out_dt == QFP4_F32) &&
+              rows32(ep.residual, ep.residual_f32);
     if (K == 0) {
-        const int grid = static_cast<int>(imin<int64_t>((M * (N / 2) + 255) / 256, 8 * num_sms()));
+        const int grid = static_cast<int>(imin<int64_t>((M * ((N + 15) / 16) + 127) / 128, 16 * num_sms()));
         if (out_dt == QFP4_F32)
-            k_epilogue_of_zero<QFP4_F32><<<grid, 256, 0, stream>>>(ep, out, static_cast<int>(M), static_cast<int>(N));
+            k_epilogue_of_zero<QFP4_F32><<<grid, 128, 0, stream>>>(ep, out, static_cast<int>(M), static_cast<int>(N));
         else
-            k_epilogue_of_zero<QFP4_BF16><<<grid, 256, 0, stream>>>(ep, out, static_cast<int>(M), static_cast<int>(N));
+            k_epilogue_of_zero<QFP4_BF16><<<grid, 128, 0, stream>>>(ep, out, static_cast<int>(M), static_cast<int>(N));
         QFP4_LAUNCH_CHECK();
         return QFP4_OK;
     }
