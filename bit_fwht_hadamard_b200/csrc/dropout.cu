@@ -88,7 +88,12 @@ __global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
             v = drop1(d, v, ww[i & 3]);
         }
-        if (act != QFP4_ACT_NONE) v *= act_slope(ld_as_float(z, DT == QFP4_F32, i), act);
+        if (act != QFP4_ACT_NONE) {
+            const float zz = ld_as_float(z, DT == QFP4_F32, i);
+            float vv[2] = {v, 0.0f}, zv[2] = {zz, 0.0f};
+            act_backward<2>(vv, zv, act);
+            v = vv[0];
+        }
         sum += v;
         st1<DT>(dz, i, v);
     }

@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[GM_STAGES], empty[GM_STAGES], acc_full, acc_empty, drain;
+    __shared__ float4 bias_sh[EP ? 2 : 1][EP ? 64 : 1];   // by tile parity
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
 
@@ -402,8 +403,14 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         for (int t = blockIdx.x; t < ntiles && !abort_flag; t += gridDim.x, ++ti) {
             int mb, nb;
             tile_coords(t, p.tiles_m, p.tiles_n, mb, nb);
+            float4 bias4 = {};
+            if constexpr (EP) bias4 = bias4_load(ep, nb * GM_BN + 128 * h + 4 * lane, p.N - nb * GM_BN - 128 * h - 4 * lane);
             if (!warp_wait(&acc_full, ti & 1)) { abort_flag = 1; break; }
             tc_fence_after();
+            if constexpr (EP) {
+                bias_sh[ti & 1][32 * h + lane] = bias4;
+                __syncwarp();
+            }
             uint32_t r[128];
             if constexpr (EP) {
                 // a lane a row: 128 columns of its own
@@ -425,7 +432,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
 
             if constexpr (EP) {
                 const int row = mb * GM_BM + 32 * q + lane;
-                if (row < p.M) ep_row128<OUT>(ep, p.out, p.N, row, nb * GM_BN + 128 * h, alpha, step, r);
+                if (row < p.M)
+                    ep_row128<OUT>(ep, p.out, p.N, row, nb * GM_BN + 128 * h, alpha, step, r, bias_sh[ti & 1] + 32 * h);
                 continue;
             }
             // r[64hh + 4j + {0,1}]: row 32q + 16hh + lane/4, columns 8j + 2(lane%4) + {0,1};
@@ -638,6 +646,7 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[G2_STAGES], empty[G2_STAGES], sfs_full[G2_SF_SLOTS], sfs_empty[G2_SF_SLOTS];
     __shared__ __align__(8) uint64_t sf_full[G2_SF_BUFS_MAX], sf_empty[G2_SF_BUFS_MAX], acc_full, acc_empty, drain;
+    __shared__ float4 bias_sh[EP ? 2 : 1][EP ? 64 : 1];   // by tile parity
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
 
@@ -863,12 +872,23 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
         for (int t = cluster; t < ntiles && !abort_flag; t += nclusters, ++ti) {
             int mb, nb;
             tile_coords(t, tiles_m, tiles_n, mb, nb);
+            float4 bias4 = {};
             if constexpr (EP) {
-                const int row = mb * G2_BM + 128 * static_cast<int>(rank) + 32 * q + lane;
-                if (ep.residual && row < p.M) ep_prefetch128(ep, p.N, row, nb * G2_BN + 128 * h);
+                const int row = mb * G2_BM + 128 * static_cast<int>(rank) + 32 * q + lane, col = nb * G2_BN + 128 * h;
+                if (ep.residual && row < p.M) ep_prefetch128(ep, p.N, row, col);
+                bias4 = bias4_load(ep, col + 4 * lane, p.N - col - 4 * lane);
             }
             if (!warp_wait(&acc_full, ti & 1)) { abort_flag = 1; break; }
             tc_fence_after();
+            // This tile's bias, once in shared memory for the four warps of a
+            // column half (each writes the same values and reads its own).
+            // acc_full of this tile says that every warp has loaded the tile
+            // before it, so none still reads the tile before that, whose
+            // buffer this is.
+            if constexpr (EP) {
+                bias_sh[ti & 1][32 * h + lane] = bias4;
+                __syncwarp();
+            }
             uint32_t r[128];
             if constexpr (EP) {
                 // a lane a row: 128 columns of its own
@@ -892,7 +912,8 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
             const int row_base = mb * G2_BM + 128 * static_cast<int>(rank);
             if constexpr (EP) {
                 const int row = row_base + 32 * q + lane;
-                if (row < p.M) ep_row128<OUT>(ep, p.out, p.N, row, nb * G2_BN + 128 * h, alpha, step, r);
+                if (row < p.M)
+                    ep_row128<OUT>(ep, p.out, p.N, row, nb * G2_BN + 128 * h, alpha, step, r, bias_sh[ti & 1] + 32 * h);
                 continue;
             }
             const int col0 = nb * G2_BN + 128 * h + 2 * (lane & 3);
@@ -1129,7 +1150,10 @@ __global__ void __launch_bounds__(128) k_epilogue_of_zero(EpParams ep, void *out
          t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t row = t / per_row;
         const int col = 16 * static_cast<int>(t % per_row), nc = imin(16, N - col);
-        ep_chunk16<OUT>(ep, out, row * N + col, col, nc, 1.0f, step, zero);
+        float4 bias[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) bias[g] = bias4_load(ep, col + 4 * g, nc - 4 * g);
+        ep_chunk16<OUT>(ep, out, row * N + col, nc, 1.0f, step, zero, bias);
     }
 }
 
