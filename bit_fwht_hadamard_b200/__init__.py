@@ -15,6 +15,7 @@ integers); ``quantize``, ``quantize_mxfp8``, ``dequantize``, ``gemm``,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import c_int, c_int64, c_size_t, c_uint64, c_void_p, c_char_p, c_double, c_float
 
@@ -523,106 +524,138 @@ def linear_backward(G, X, W, fmt=NVFP4, seed=0, out_dtype=None, want_dx=True, wa
 
 
 # ------------------------------------------------------------------ around a linear layer
-def _tensor(t, name, like, shape=None, dtype=None):
-    """Checks of a tensor that goes to the C ABI beside `like`: CUDA,
-    contiguous, on the same device, and of the given shape and dtype."""
-    _input(t, name, dims=None)
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, not {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+# These wrappers check every tensor they hand over; a call on a few rows costs
+# about as much in Python as on the device, so the checks are one expression
+# where they pass and name the fault only where they fail.
+_current_device = None      # torch.cuda.current_device
+_raw_stream = None          # device index -> handle of its current stream
 
 
-def _param_dt(t, name):
+def _cuda_api():
+    global _current_device, _raw_stream
     torch = _torch()
-    if t is None or t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype == torch.float32:
-        return F32
+    _current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
+def _tensor(t, name, index, shape=None, dtype=None):
+    """Checks of a tensor that goes to the C ABI: CUDA, contiguous, on device
+    `index`, and of the given shape and dtype; its address."""
+    if not (t.is_cuda and t.is_contiguous() and t.get_device() == index and (shape is None or t.shape == shape)
+            and (dtype is None or t.dtype is dtype)):
+        _input(t, name, dims=None)
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, not {t.device}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+def _param(t, name, index, shape):
+    """(address, C type) of a bf16 or fp32 parameter, or (None, BF16)."""
+    if t is None:
+        return None, BF16
+    torch = _torch()
+    p = _tensor(t, name, index, shape)
+    if t.dtype is torch.bfloat16:
+        return p, BF16
+    if t.dtype is torch.float32:
+        return p, F32
     raise TypeError(f"{name} must be bfloat16 or float32")
 
 
-def _step(step, like):
+def _step(step, index):
     """The dropout's step counter: None, or a one-element int64 CUDA tensor."""
     if step is None:
         return None
-    _tensor(step, "step", like, dtype=_torch().int64)
+    p = _tensor(step, "step", index, None, _torch().int64)
     if step.numel() != 1:
         raise ValueError("step must have one element")
-    return step.data_ptr()
-
-
-class _launch_on:
-    """Runs a call on `like`'s device (the C ABI launches on the current one)
-    and on `stream` there (default: that device's current stream), as an
-    integer handle."""
-
-    def __init__(self, like, stream):
-        torch = _torch()
-        self._guard = None
-        if like.device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(like.device)
-        self._like, self._stream = like, stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        if self._stream is None:
-            return _torch().cuda.current_stream().cuda_stream
-        return self._stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+    return p
 
 
 def _new(shape, dtype, like, stream):
     """A fresh tensor on `like`'s device, of the allocator's pool for the
     stream that the call runs on (its memory may still be in use elsewhere
     on any other)."""
-    torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+    with _torch().cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _operand(q, name, rows, K, fmt, like):
+def _call(fn, index, stream, *args):
+    """fn(*args, stream) on device `index` (the C ABI launches on the current
+    one) and `stream` (default: that device's current stream)."""
+    if _raw_stream is None:
+        _cuda_api()
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with _torch().cuda.device(index):
+            st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if st != OK:
+        raise QFP4Error(st, fn.__name__)
+
+
+_gemm_epilogue_ws = functools.lru_cache(1024)(qfp4_gemm_epilogue_workspace_bytes)
+_linear_forward_ws = functools.lru_cache(1024)(qfp4_linear_forward_workspace_bytes)
+_epilogue_backward_ws = functools.lru_cache(1024)(qfp4_epilogue_backward_workspace_bytes)
+_layernorm_backward_ws = functools.lru_cache(1024)(qfp4_layernorm_backward_workspace_bytes)
+
+
+def _scratch(workspace, nbytes, like, stream):
+    """(address, bytes, the tensor that has to live until the call) of the
+    caller's workspace, or of a fresh one."""
+    if workspace is None:
+        if not nbytes:
+            return None, 0, None
+        workspace = _new((nbytes,), _torch().uint8, like, stream)
+    return workspace.data_ptr(), workspace.nbytes, workspace
+
+
+def _operand(q, name, rows, K, fmt, index):
+    """Addresses of codes, scales and tensor scale."""
     torch = _torch()
-    g = 16 if fmt == NVFP4 else 32
-    _tensor(q["codes"], f"{name} codes", like, (rows, K if fmt == MXFP8 else K // 2), torch.uint8)
-    _tensor(q["scales"], f"{name} scales", like, (rows, K // g), torch.uint8)
-    if fmt == NVFP4:
-        _tensor(q["tscale"], f"{name} tscale", like, dtype=torch.float32)
+    u8 = torch.uint8
+    c = _tensor(q["codes"], f"{name} codes", index, (rows, K if fmt == MXFP8 else K // 2), u8)
+    s = _tensor(q["scales"], f"{name} scales", index, (rows, K // (16 if fmt == NVFP4 else 32)), u8)
+    return c, s, _tensor(q["tscale"], f"{name} tscale", index, None, torch.float32) if fmt == NVFP4 else None
 
 
-def _epilogue(M, N, out, bias, act, want_preact, dropout_p, seed, step, residual, stream):
-    """(Epilogue struct, preact tensor or None) for outputs like `out`."""
+def _output(out, shape, out_dtype, like, index, stream):
+    """(tensor, address, C type) of a bf16 or fp32 output."""
+    torch = _torch()
+    if out is None:
+        out = _new(shape, torch.float32 if out_dtype is None else out_dtype, like, stream)
+        p = out.data_ptr()
+    else:
+        p = _tensor(out, "out", index, shape)
+    if out.dtype is torch.float32:
+        return out, p, F32
+    if out.dtype is torch.bfloat16:
+        return out, p, BF16
+    raise TypeError("outputs are bfloat16 or float32")
+
+
+def _epilogue(shape, out, index, bias, act, want_preact, dropout_p, seed, step, residual, stream):
+    """(Epilogue struct, preact tensor or None) for an output tensor."""
     e = Epilogue()
     e.act = act
     if bias is not None:
-        _tensor(bias, "bias", out, (N,))
-        e.bias, e.bias_dt = bias.data_ptr(), _param_dt(bias, "bias")
+        e.bias, e.bias_dt = _param(bias, "bias", index, shape[1:])
     if residual is not None:
-        _tensor(residual, "residual", out, (M, N))
-        e.residual, e.residual_dt = residual.data_ptr(), _param_dt(residual, "residual")
+        e.residual, e.residual_dt = _param(residual, "residual", index, shape)
     preact = None
-    if want_preact is not False and want_preact is not None:
-        preact = _new((M, N), out.dtype, out, stream) if want_preact is True else want_preact
-        _tensor(preact, "preact", out, (M, N), out.dtype)
+    if want_preact is True:
+        preact = _new(shape, out.dtype, out, stream)
         e.preact = preact.data_ptr()
-    e.dropout_p, e.seed, e.step = dropout_p, seed & ((1 << 64) - 1), _step(step, out)
+    elif want_preact is not False and want_preact is not None:
+        preact = want_preact
+        e.preact = _tensor(preact, "preact", index, shape, out.dtype)
+    if dropout_p or step is not None:
+        e.dropout_p, e.seed, e.step = dropout_p, seed & ((1 << 64) - 1), _step(step, index)
     return e, preact
-
-
-def _out_dt(out):
-    """The C type of an output tensor."""
-    torch = _torch()
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("outputs are bfloat16 or float32")
-    return F32 if out.dtype == torch.float32 else BF16
 
 
 def gemm_epilogue(A, B, M, N, K, fmt, bias=None, act=ACT_NONE, want_preact=False, dropout_p=0.0, seed=0, step=None,
@@ -632,24 +665,16 @@ def gemm_epilogue(A, B, M, N, K, fmt, bias=None, act=ACT_NONE, want_preact=False
     ``quantize_mxfp8``.  ``want_preact``: True (or a buffer) to keep the sum
     before the activation for ``epilogue_backward``, else preact is None.
     ``step``: a one-element int64 CUDA tensor, the dropout's counter."""
-    torch = _torch()
     like = B["codes"]
-    _operand(A, "A", M, K, fmt, like)
-    _operand(B, "B", N, K, fmt, like)
-    if out is None:
-        out = _new((M, N), torch.float32 if out_dtype is None else out_dtype, like, stream)
-    else:
-        _tensor(out, "out", like, (M, N))
-    dt = _out_dt(out)
-    e, preact = _epilogue(M, N, out, bias, act, want_preact, dropout_p, seed, step, residual, stream)
-    wsb = qfp4_gemm_epilogue_workspace_bytes(M, N, K, fmt)
-    if workspace is None and wsb:
-        workspace = _new((wsb,), torch.uint8, like, stream)
-    with _launch_on(like, stream) as s:
-        st = qfp4_gemm_epilogue(_ptr(A["codes"]), _ptr(A["scales"]), _ptr(A.get("tscale")), _ptr(B["codes"]),
-                                _ptr(B["scales"]), _ptr(B.get("tscale")), M, N, K, fmt, e, dt, _ptr(out),
-                                _ptr(workspace), workspace.nbytes if workspace is not None else 0, s)
-    _check(st, "qfp4_gemm_epilogue")
+    _input(like, "B codes")
+    index = like.get_device()
+    ac, sa, ta = _operand(A, "A", M, K, fmt, index)
+    bc, sb, tb = _operand(B, "B", N, K, fmt, index)
+    shape = (M, N)
+    out, po, dt = _output(out, shape, out_dtype, like, index, stream)
+    e, preact = _epilogue(shape, out, index, bias, act, want_preact, dropout_p, seed, step, residual, stream)
+    ws, wsb, keep = _scratch(workspace, _gemm_epilogue_ws(M, N, K, fmt), like, stream)
+    _call(qfp4_gemm_epilogue, index, stream, ac, sa, ta, bc, sb, tb, M, N, K, fmt, e, dt, po, ws, wsb)
     return out, preact
 
 
@@ -657,26 +682,18 @@ def linear_forward_epilogue(X, W, fmt=NVFP4, four6=False, bias=None, act=ACT_NON
                             seed=0, step=None, residual=None, out_dtype=None, out=None, workspace=None, stream=None):
     """``linear_forward`` with the epilogue of ``gemm_epilogue``
     (qfp4_linear_forward_epilogue); returns (Y, preact)."""
-    torch = _torch()
+    bf16 = _torch().bfloat16
     _input(X, "X")
     _input(W, "W")
+    index = X.get_device()
     M, K = X.shape
     N = W.shape[0]
-    _tensor(X, "X", W, (M, W.shape[1]), torch.bfloat16)
-    _tensor(W, "W", X, dtype=torch.bfloat16)
-    if out is None:
-        out = _new((M, N), torch.float32 if out_dtype is None else out_dtype, X, stream)
-    else:
-        _tensor(out, "out", X, (M, N))
-    dt = _out_dt(out)
-    e, preact = _epilogue(M, N, out, bias, act, want_preact, dropout_p, seed, step, residual, stream)
-    wsb = qfp4_linear_forward_workspace_bytes(M, N, K, fmt)
-    if workspace is None and wsb:
-        workspace = _new((wsb,), torch.uint8, X, stream)
-    with _launch_on(X, stream) as s:
-        st = qfp4_linear_forward_epilogue(_ptr(X), _ptr(W), M, N, K, fmt, int(four6), e, dt, _ptr(out),
-                                          _ptr(workspace), workspace.nbytes if workspace is not None else 0, s)
-    _check(st, "qfp4_linear_forward_epilogue")
+    px, pw = _tensor(X, "X", index, None, bf16), _tensor(W, "W", index, (N, K), bf16)
+    shape = (M, N)
+    out, po, dt = _output(out, shape, out_dtype, X, index, stream)
+    e, preact = _epilogue(shape, out, index, bias, act, want_preact, dropout_p, seed, step, residual, stream)
+    ws, wsb, keep = _scratch(workspace, _linear_forward_ws(M, N, K, fmt), X, stream)
+    _call(qfp4_linear_forward_epilogue, index, stream, px, pw, M, N, K, fmt, int(four6), e, dt, po, ws, wsb)
     return out, preact
 
 
@@ -686,30 +703,26 @@ def epilogue_backward(dY, Z=None, act=ACT_NONE, dropout_p=0.0, seed=0, step=None
     (qfp4_epilogue_backward): dY (M, N) and the forward's preact Z, bf16 or
     fp32; dZ of their type, dbias (N,) fp32 or None.  ``out`` may supply a
     dict with dZ and dbias."""
-    torch = _torch()
     _input(dY, "dY")
-    M, N = dY.shape
+    index, shape, dtype = dY.get_device(), dY.shape, dY.dtype
+    M, N = shape
     dt = _xdt(dY)
-    if Z is not None:
-        _tensor(Z, "Z", dY, (M, N), dY.dtype)
-    o = dict(out) if out is not None else {}
-    if "dZ" not in o:
-        o["dZ"] = _new((M, N), dY.dtype, dY, stream)
-    if want_dbias and "dbias" not in o:
-        o["dbias"] = _new((N,), torch.float32, dY, stream)
-    _tensor(o["dZ"], "dZ", dY, (M, N), dY.dtype)
-    db = o.get("dbias")
+    pz = None if Z is None else _tensor(Z, "Z", index, shape, dtype)
+    dZ = db = pb = ws = keep = None
     wsb = 0
+    if out is not None:
+        dZ, db = out.get("dZ"), out.get("dbias")
+    if dZ is None:
+        dZ = _new(shape, dtype, dY, stream)
+    pd = _tensor(dZ, "dZ", index, shape, dtype)
+    if db is None and want_dbias:
+        db = _new((N,), _torch().float32, dY, stream)
     if db is not None:
-        _tensor(db, "dbias", dY, (N,), torch.float32)
-        wsb = qfp4_epilogue_backward_workspace_bytes(M, N)
-        if workspace is None and wsb:
-            workspace = _new((wsb,), torch.uint8, dY, stream)
-    with _launch_on(dY, stream) as s:
-        st = qfp4_epilogue_backward(_ptr(dY), _ptr(Z), dt, M, N, act, dropout_p, seed, _step(step, dY), _ptr(o["dZ"]),
-                                    _ptr(db), _ptr(workspace), workspace.nbytes if workspace is not None else 0, s)
-    _check(st, "qfp4_epilogue_backward")
-    return o["dZ"], db
+        pb = _tensor(db, "dbias", index, (N,), _torch().float32)
+        ws, wsb, keep = _scratch(workspace, _epilogue_backward_ws(M, N), dY, stream)
+    _call(qfp4_epilogue_backward, index, stream, dY.data_ptr(), pz, dt, M, N, act, dropout_p, seed,
+          _step(step, index), pd, pb, ws, wsb)
+    return dZ, db
 
 
 def dropout(x, p, seed=0, step=None, residual=None, out=None, stream=None):
@@ -717,26 +730,25 @@ def dropout(x, p, seed=0, step=None, residual=None, out=None, stream=None):
     plus the residual (qfp4_dropout); x bf16 or fp32 of any shape.  The same
     call on the output's gradient is the backward pass."""
     _input(x, "x", dims=None)
+    index = x.get_device()
     dt = _xdt(x)
-    if residual is not None:
-        _tensor(residual, "residual", x, x.shape, x.dtype)
+    pr = None if residual is None else _tensor(residual, "residual", index, x.shape, x.dtype)
     if out is None:
         out = _new(x.shape, x.dtype, x, stream)
+        po = out.data_ptr()
     else:
-        _tensor(out, "out", x, x.shape, x.dtype)
-    with _launch_on(x, stream) as s:
-        st = qfp4_dropout(_ptr(x), dt, x.numel(), p, seed, _step(step, x), _ptr(residual), _ptr(out), s)
-    _check(st, "qfp4_dropout")
+        po = _tensor(out, "out", index, x.shape, x.dtype)
+    _call(qfp4_dropout, index, stream, x.data_ptr(), dt, x.numel(), p, seed, _step(step, index), pr, po)
     return out
 
 
-def _norm_params(x, D, gamma, beta):
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            _tensor(t, name, x, (D,))
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+def _norm_params(index, D, gamma, beta):
+    """(gamma's address, beta's, their one C type)."""
+    pg, gdt = _param(gamma, "gamma", index, (D,))
+    pb, bdt = _param(beta, "beta", index, (D,))
+    if gamma is not None and beta is not None and gdt != bdt:
         raise TypeError("gamma and beta must have one dtype")
-    return _param_dt(gamma if gamma is not None else beta, "gamma and beta")
+    return pg, pb, bdt if gamma is None else gdt
 
 
 def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, want_stats=True, out=None, stream=None):
@@ -744,57 +756,62 @@ def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, want_stats=True, out=N
     (qfp4_layernorm_forward); gamma and beta (D,) bf16 or fp32, or None; mean
     and rstd (M,) fp32, or None without ``want_stats``.  ``out`` may supply a
     dict with y, mean and rstd."""
-    torch = _torch()
     _input(x, "x")
-    M, D = x.shape
-    dt, wdt = _xdt(x), _norm_params(x, D, gamma, beta)
-    o = dict(out) if out is not None else {}
-    if "y" not in o:
-        o["y"] = _new((M, D), x.dtype, x, stream)
-    _tensor(o["y"], "y", x, (M, D), x.dtype)
-    for k in ("mean", "rstd"):
-        if k not in o and want_stats:
-            o[k] = _new((M,), torch.float32, x, stream)
-        if o.get(k) is not None:
-            _tensor(o[k], k, x, (M,), torch.float32)
-    with _launch_on(x, stream) as s:
-        st = qfp4_layernorm_forward(_ptr(x), dt, M, D, _ptr(gamma), _ptr(beta), wdt, eps, _ptr(o["y"]),
-                                    _ptr(o.get("mean")), _ptr(o.get("rstd")), s)
-    _check(st, "qfp4_layernorm_forward")
-    return o["y"], o.get("mean"), o.get("rstd")
+    index, shape = x.get_device(), x.shape
+    M, D = shape
+    dt = _xdt(x)
+    pg, pb, wdt = _norm_params(index, D, gamma, beta)
+    f32 = _torch().float32
+    if out is None:
+        y = _new(shape, x.dtype, x, stream)
+        py, mean, rstd, pm, pr = y.data_ptr(), None, None, None, None
+        if want_stats:
+            mean, rstd = _new((M,), f32, x, stream), _new((M,), f32, x, stream)
+            pm, pr = mean.data_ptr(), rstd.data_ptr()
+    else:
+        y, mean, rstd = out.get("y"), out.get("mean"), out.get("rstd")
+        if y is None:
+            y = _new(shape, x.dtype, x, stream)
+        if mean is None and want_stats:
+            mean = _new((M,), f32, x, stream)
+        if rstd is None and want_stats:
+            rstd = _new((M,), f32, x, stream)
+        py = _tensor(y, "y", index, shape, x.dtype)
+        pm = None if mean is None else _tensor(mean, "mean", index, (M,), f32)
+        pr = None if rstd is None else _tensor(rstd, "rstd", index, (M,), f32)
+    _call(qfp4_layernorm_forward, index, stream, x.data_ptr(), dt, M, D, pg, pb, wdt, eps, py, pm, pr)
+    return y, mean, rstd
 
 
 def layernorm_backward(dy, x, gamma, mean, rstd, want_dx=True, want_dw=True, out=None, workspace=None, stream=None):
     """(dx, dgamma, dbeta) of ``layernorm_forward`` (qfp4_layernorm_backward);
     dx of x's type, dgamma and dbeta (D,) fp32; None for what is not wanted.
     ``out`` may supply a dict with dx, dgamma and dbeta."""
-    torch = _torch()
     _input(x, "x")
-    M, D = x.shape
-    dt, wdt = _xdt(x), _norm_params(x, D, gamma, None)
-    _tensor(dy, "dy", x, (M, D), x.dtype)
-    _tensor(mean, "mean", x, (M,), torch.float32)
-    _tensor(rstd, "rstd", x, (M,), torch.float32)
-    o = dict(out) if out is not None else {}
-    if want_dx and "dx" not in o:
-        o["dx"] = _new((M, D), x.dtype, x, stream)
-    if o.get("dx") is not None:
-        _tensor(o["dx"], "dx", x, (M, D), x.dtype)
+    index, shape, dtype = x.get_device(), x.shape, x.dtype
+    M, D = shape
+    dt = _xdt(x)
+    f32 = _torch().float32
+    pg, _, wdt = _norm_params(index, D, gamma, None)
+    py = _tensor(dy, "dy", index, shape, dtype)
+    pm, pr = _tensor(mean, "mean", index, (M,), f32), _tensor(rstd, "rstd", index, (M,), f32)
+    dx = dg = db = ws = keep = None
     wsb = 0
-    for k in ("dgamma", "dbeta"):
-        if want_dw and k not in o:
-            o[k] = _new((D,), torch.float32, x, stream)
-        if o.get(k) is not None:
-            _tensor(o[k], k, x, (D,), torch.float32)
-            wsb = qfp4_layernorm_backward_workspace_bytes(M, D)
-    if workspace is None and wsb:
-        workspace = _new((wsb,), torch.uint8, x, stream)
-    with _launch_on(x, stream) as s:
-        st = qfp4_layernorm_backward(_ptr(dy), _ptr(x), dt, M, D, _ptr(gamma), wdt, _ptr(mean), _ptr(rstd),
-                                     _ptr(o.get("dx")), _ptr(o.get("dgamma")), _ptr(o.get("dbeta")), _ptr(workspace),
-                                     workspace.nbytes if workspace is not None else 0, s)
-    _check(st, "qfp4_layernorm_backward")
-    return o.get("dx"), o.get("dgamma"), o.get("dbeta")
+    if out is not None:
+        dx, dg, db = out.get("dx"), out.get("dgamma"), out.get("dbeta")
+    if dx is None and want_dx:
+        dx = _new(shape, dtype, x, stream)
+    if dg is None and want_dw:
+        dg = _new((D,), f32, x, stream)
+    if db is None and want_dw:
+        db = _new((D,), f32, x, stream)
+    px = None if dx is None else _tensor(dx, "dx", index, shape, dtype)
+    pdg = None if dg is None else _tensor(dg, "dgamma", index, (D,), f32)
+    pdb = None if db is None else _tensor(db, "dbeta", index, (D,), f32)
+    if dg is not None or db is not None:
+        ws, wsb, keep = _scratch(workspace, _layernorm_backward_ws(M, D), x, stream)
+    _call(qfp4_layernorm_backward, index, stream, py, x.data_ptr(), dt, M, D, pg, wdt, pm, pr, px, pdg, pdb, ws, wsb)
+    return dx, dg, db
 
 
 def kl_calibrate(x, bins=2048, levels=8, grid=0, stream=None, out=None):

@@ -1,57 +1,65 @@
 // dropout.cu -- dropout from Philox words (no stored mask), optionally added
 // to a residual, and the backward pass of the GEMM's epilogue (dropout,
 // activation, bias).
-#include "epilogue.cuh"
+#include "vec.cuh"
 
 namespace qfp4 {
 
-// Four consecutive elements as binary32, and back.
-template <int DT>
-__device__ __forceinline__ float4 ld4(const void *p, int64_t i)   // 4-element aligned
+// Dropout of V values whose first one is element i (i % 4 == 0).
+template <int V>
+__device__ __forceinline__ void drop_values(const DropParams &d, uint64_t step, int64_t i, float *v)
 {
-    if (DT == QFP4_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
-    return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-}
-template <int DT>
-__device__ __forceinline__ void st4(void *p, int64_t i, float4 v)
-{
-    if (DT == QFP4_F32) *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = v;
-    else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
-            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-}
-template <int DT>
-__device__ __forceinline__ void st1(void *p, int64_t i, float v)
-{
-    if (DT == QFP4_F32) static_cast<float *>(p)[i] = v;
-    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+#pragma unroll
+    for (int g = 0; g < V / 4; ++g) {
+        const uint4 w = drop_words4(d, step, (static_cast<uint64_t>(i) >> 2) + g);
+        v[4 * g] = drop1(d, v[4 * g], w.x);
+        v[4 * g + 1] = drop1(d, v[4 * g + 1], w.y);
+        v[4 * g + 2] = drop1(d, v[4 * g + 2], w.z);
+        v[4 * g + 3] = drop1(d, v[4 * g + 3], w.w);
+    }
 }
 
 // ------------------------------------------------------------------ dropout
+// A thread takes U vectors of 16 bytes, a block's width apart, with all their
+// loads first.
+constexpr int DROP_U = 2;
 template <int DT, bool RES>
 __global__ void __launch_bounds__(256) k_dropout(const void *x, const void *res, int64_t n, DropParams d, void *out)
 {
+    constexpr int V = DT == QFP4_F32 ? 4 : 8;
+    pdl_wait();
+    pdl_trigger();
     const uint64_t step = drop_step(d);
-    const int64_t nth = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t qd = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; qd < (n + 3) / 4; qd += nth) {
-        uint4 w = make_uint4(~0u, ~0u, ~0u, ~0u);
-        if (d.on) w = drop_words4(d, step, static_cast<uint64_t>(qd));
-        const int64_t i = 4 * qd;
-        if (i + 4 <= n) {
-            float4 v = ld4<DT>(x, i);
-            v = make_float4(drop1(d, v.x, w.x), drop1(d, v.y, w.y), drop1(d, v.z, w.z), drop1(d, v.w, w.w));
+    const int64_t vec0 = static_cast<int64_t>(blockIdx.x) * (256 * DROP_U) + threadIdx.x, nvec = n / V;
+    Vec<DT, V> a[DROP_U], r[DROP_U];
+#pragma unroll
+    for (int u = 0; u < DROP_U; ++u)
+        if (vec0 + 256 * u < nvec) {
+            a[u].load(x, (vec0 + 256 * u) * V);
+            if (RES) r[u].load(res, (vec0 + 256 * u) * V);
+        }
+#pragma unroll
+    for (int u = 0; u < DROP_U; ++u) {
+        const int64_t vec = vec0 + 256 * u, i = vec * V;
+        float v[V], s[V];
+        if (vec < nvec) {
+            a[u].get(v);
+            if (d.on) drop_values<V>(d, step, i, v);
             if (RES) {
-                const float4 r = ld4<DT>(res, i);
-                v = make_float4(v.x + r.x, v.y + r.y, v.z + r.z, v.w + r.w);
+                r[u].get(s);
+#pragma unroll
+                for (int t = 0; t < V; ++t) v[t] += s[t];
             }
-            st4<DT>(out, i, v);
-        } else {
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            for (int t = 0; i + t < n; ++t) {
-                float v = drop1(d, ld_as_float(x, DT == QFP4_F32, i + t), ww[t]);
-                if (RES) v += ld_as_float(res, DT == QFP4_F32, i + t);
-                st1<DT>(out, i + t, v);
+            a[u].set(v);
+            a[u].store(out, i);
+        } else if (vec == nvec && i < n) {                  // the last, partial vector
+            for (int t = 0; t < V; ++t) v[t] = i + t < n ? ld_as_float(x, DT == QFP4_F32, i + t) : 0.0f;
+            if (d.on) drop_values<V>(d, step, i, v);
+            for (int t = 0; t < V && i + t < n; ++t) {
+                if (RES) v[t] += ld_as_float(res, DT == QFP4_F32, i + t);
+                Vec<DT, 1> one;
+                one.set(v + t);
+                one.store(out, i + t);
             }
         }
     }
@@ -60,81 +68,185 @@ __global__ void __launch_bounds__(256) k_dropout(const void *x, const void *res,
 template <int DT>
 static int launch_dropout(const void *x, const void *res, int64_t n, const DropParams &d, void *out, cudaStream_t s)
 {
-    const int grid = static_cast<int>(imin<int64_t>(((n + 3) / 4 + 255) / 256, 8 * num_sms()));
-    if (res) k_dropout<DT, true><<<grid, 256, 0, s>>>(x, res, n, d, out);
-    else k_dropout<DT, false><<<grid, 256, 0, s>>>(x, res, n, d, out);
+    const int64_t per = 256 * DROP_U * (DT == QFP4_F32 ? 4 : 8);
+    const dim3 grid(static_cast<unsigned>((n + per - 1) / per));
+    const cudaError_t e = res ? launch_pdl(k_dropout<DT, true>, grid, dim3(256), 0, s, x, res, n, d, out)
+                              : launch_pdl(k_dropout<DT, false>, grid, dim3(256), 0, s, x, res, n, d, out);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
+}
+
+// ------------------------------------------------------------------ column sums of partial rows
+// out[c] = sum over the rows r of partial[r][c] (in a fixed order): 32 columns
+// x 32 row lanes a block.  A row of partial is `tiles` tiles of TW + V columns:
+// slot V + j of tile t belongs to column t TW + j, j >= -V (V = 0: plain rows
+// of TW = N columns).  blockIdx.y selects one of up to two outputs, whose
+// partial rows follow one another.
+__global__ void __launch_bounds__(1024) k_column_sums(const float *partial, int rows, int64_t N, int TW, int V, int tiles,
+                                                       float *out0, float *out1)
+{
+    __shared__ float red[32][33];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    float *out = blockIdx.y ? out1 : out0;
+    if (!out) return;
+    const int64_t stride = static_cast<int64_t>(tiles) * (TW + V);
+    const float *src = partial + static_cast<int64_t>(blockIdx.y) * rows * stride;
+    float s = 0.0f;
+    if (c < N) {
+        const int tile = static_cast<int>(c / TW), j = static_cast<int>(c - static_cast<int64_t>(tile) * TW);
+        const float *p = src + static_cast<int64_t>(tile) * (TW + V) + V + j;
+        const bool two = j >= TW - V && tile + 1 < tiles;       // the next tile's warps may hold this column too
+#pragma unroll 4
+        for (int r = w; r < rows; r += 32) {
+            s += p[r * stride];
+            if (two) s += p[r * stride + V];                     // slot j - TW + V of the next tile
+        }
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    const float t = warp_sum(red[lane][w]);                      // warp w: column w of the block
+    const int64_t cw = static_cast<int64_t>(blockIdx.x) * 32 + w;
+    if (lane == 0 && cw < N) out[cw] = t;
+}
+
+static int column_sums(const float *partial, int64_t rows, int64_t N, int TW, int V, int tiles, float *out0,
+                       float *out1, bool two, cudaStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>((N + 31) / 32), two ? 2 : 1);
+    if (launch_pdl(k_column_sums, grid, dim3(1024), 0, s, partial, static_cast<int>(rows), N, TW, V, tiles, out0,
+                   out1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
     QFP4_LAUNCH_CHECK();
     return QFP4_OK;
 }
 
 // ------------------------------------------------------------------ epilogue backward
-// One thread a column and row chunk: dz = drop(dy) act'(z), and the chunk's
-// column sum into partial[chunk][N].
+// A warp takes one row at a time, eight rows apart, and a lane V = 16 bytes of
+// columns, so that each lane keeps the sums of its own columns in registers.
+// Vectors are aligned in memory, not in the row: a row of N columns starts
+// off = (m N) mod V elements into a vector, the same for all rows that a warp
+// takes (V divides 8), so its lanes' columns stay the same and any N runs on
+// 16-byte accesses; the vectors that straddle a row's ends go element by
+// element.  Reads dY and Z once, writes dZ once: bound by memory.
+constexpr int EB_TILE = 32;                                   // vectors of a block's column tile
+
+// Grid of the kernel: column tiles, row chunks (each a multiple of eight
+// rows) for about six blocks an SM.
+struct EbGrid {
+    int tiles, chunks;
+    int64_t rows;
+};
+static EbGrid epilogue_backward_grid(int64_t M, int64_t N, int V)
+{
+    EbGrid g;
+    const int64_t tw = EB_TILE * V;
+    g.tiles = static_cast<int>((N % V ? N + V - 1 : N) / tw + ((N % V ? N + V - 1 : N) % tw != 0));
+    const int64_t want = imax<int64_t>(1, imin<int64_t>((6 * 148 + g.tiles - 1) / g.tiles, 512));
+    g.rows = ((M + want - 1) / want + 7) / 8 * 8;
+    g.chunks = static_cast<int>((M + g.rows - 1) / g.rows);
+    return g;
+}
+
 template <int DT>
 __global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const void *z, int64_t M, int64_t N,
                                                             int64_t rows, int act, DropParams d, void *dz,
                                                             float *partial)
 {
+    constexpr int V = DT == QFP4_F32 ? 4 : 8, U = 2, TW = EB_TILE * V;
+    __shared__ float red[8][TW + V];
+    pdl_wait();
+    pdl_trigger();
     const uint64_t step = drop_step(d);
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (c >= N) return;
-    const int64_t m0 = blockIdx.y * rows, m1 = imin(M, m0 + rows);
-    float sum = 0.0f;
-    for (int64_t m = m0; m < m1; ++m) {
-        const int64_t i = m * N + c;
-        float v = ld_as_float(dy, DT == QFP4_F32, i);
-        if (d.on) {
-            const uint4 w = drop_words4(d, step, static_cast<uint64_t>(i) >> 2);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-            v = drop1(d, v, ww[i & 3]);
-        }
-        if (act != QFP4_ACT_NONE) {
-            const float zz = ld_as_float(z, DT == QFP4_F32, i);
-            float vv[2] = {v, 0.0f}, zv[2] = {zz, 0.0f};
-            act_backward<2>(vv, zv, act);
-            v = vv[0];
-        }
-        sum += v;
-        st1<DT>(dz, i, v);
-    }
-    if (partial) partial[blockIdx.y * N + c] = sum;
-}
-
-// out[c] = sum over the rows of partial (rows x N), in a fixed order: 32
-// columns x 8 row lanes a block.  blockIdx.y selects one of up to two arrays.
-__global__ void __launch_bounds__(256) k_column_sums(const float *partial, int64_t rows, int64_t N, float *out0,
-                                                      float *out1)
-{
-    __shared__ float red[8][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    float *out = blockIdx.y ? out1 : out0;
-    const float *src = partial + blockIdx.y * rows * N;
-    float s = 0.0f;
-    if (c < N)
-        for (int64_t r = w; r < rows; r += 8) s += src[r * N + c];
-    red[w][lane] = s;
+    const int off = static_cast<int>((w * (N & 7)) & (V - 1));
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * TW + lane * V - off;   // this lane's first column
+    const bool full = c0 >= 0 && c0 + V <= N, some = c0 + V > 0 && c0 < N;
+    const int64_t m0 = blockIdx.y * rows, m1 = imin(M, m0 + rows);
+    const bool use_z = act != QFP4_ACT_NONE;
+    float sum[V];
+#pragma unroll
+    for (int t = 0; t < V; ++t) sum[t] = 0.0f;
+    for (int64_t m = m0 + w; m < m1; m += 8 * U) {
+        Vec<DT, V> g[U], a[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = (m + 8 * u) * N + c0;
+            if (m + 8 * u < m1 && full) {
+                g[u].load(dy, i);
+                if (use_z) a[u].load(z, i);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[u].r[k] = a[u].r[k] = 0u;
+                if (m + 8 * u < m1 && some) {
+#pragma unroll
+                    for (int t = 0; t < V; ++t)
+                        if (c0 + t >= 0 && c0 + t < N) {
+                            g[u].load1(dy, i, t);
+                            if (use_z) a[u].load1(z, i, t);
+                        }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (m + 8 * u >= m1 || !some) continue;
+            const int64_t i = (m + 8 * u) * N + c0;             // a multiple of V; may be -V + 1 .. -1 only with off
+            float v[V], x[V];
+            g[u].get(v);
+            if (d.on) drop_values<V>(d, step, i, v);
+            if (use_z) {
+                a[u].get(x);
+                act_backward<V>(v, x, act);
+            }
+#pragma unroll
+            for (int t = 0; t < V; ++t) sum[t] += v[t];         // zero outside the row
+            g[u].set(v);
+            if (full) g[u].store(dz, i);
+            else {
+#pragma unroll
+                for (int t = 0; t < V; ++t)
+                    if (c0 + t >= 0 && c0 + t < N) g[u].store1(dz, i, t);
+            }
+        }
+    }
+    if (!partial) return;
+    // slot V + j of red: column blockIdx.x TW + j; a warp covers j = -off .. TW - off - 1
+    for (int j = lane; j < V; j += 32) red[w][j] = red[w][TW + j] = 0.0f;
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < V; ++t) red[w][V + lane * V + t - off] = sum[t];
     __syncthreads();
-    if (w == 0 && c < N && out) {
-        for (int k = 1; k < 8; ++k) s += red[k][lane];
-        out[c] = s;
+    float *dst = partial + (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * (TW + V);
+    for (int j = threadIdx.x; j < TW + V; j += 256) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += red[k][j];
+        dst[j] = s;
     }
 }
 
-static int column_sums(const float *partial, int64_t rows, int64_t N, float *out0, float *out1, bool two,
-                       cudaStream_t s)
+template <int DT>
+static int epilogue_backward(const void *dY, const void *Z, int64_t M, int64_t N, int act, const DropParams &d,
+                             void *dZ, float *dbias, float *partial, cudaStream_t s)
 {
-    k_column_sums<<<dim3(static_cast<unsigned>((N + 31) / 32), two ? 2 : 1), 256, 0, s>>>(partial, rows, N, out0, out1);
+    constexpr int V = DT == QFP4_F32 ? 4 : 8;
+    const EbGrid g = epilogue_backward_grid(M, N, V);
+    if (launch_pdl(k_epilogue_backward<DT>, dim3(g.tiles, g.chunks), dim3(256), 0, s, dY, Z, M, N, g.rows, act, d, dZ,
+                   dbias ? partial : nullptr) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
     QFP4_LAUNCH_CHECK();
-    return QFP4_OK;
-}
-
-// Row chunks of the epilogue's backward pass: enough blocks for four waves
-// of the device, at most 512 (the partial sums' rows).
-static int64_t epilogue_chunks(int64_t M, int64_t N)
-{
-    const int64_t cols = (N + 255) / 256;
-    return imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));
+    return dbias ? column_sums(partial, g.chunks, N, EB_TILE * V, V, g.tiles, dbias, nullptr, false, s) : QFP4_OK;
 }
 
 }  // namespace qfp4
@@ -148,8 +260,7 @@ extern "C" int qfp4_dropout(const void *x, qfp4_dtype dt, int64_t n, double p, u
     if (!dropout_ok(p)) return QFP4_ERR_ARG;
     if (n < 0 || n > (int64_t(1) << 38)) return QFP4_ERR_SHAPE;
     if (n > 0 && (!x || !out)) return QFP4_ERR_ARG;
-    if (!aligned16(x) || !aligned16(residual) || !aligned16(out) || !step_aligned(step))
-        return QFP4_ERR_ALIGN;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(out) || !step_aligned(step)) return QFP4_ERR_ALIGN;
     if (n == 0) return QFP4_OK;
     const DropParams d = drop_params(p, seed, step);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -160,7 +271,12 @@ extern "C" int qfp4_dropout(const void *x, qfp4_dtype dt, int64_t n, double p, u
 extern "C" size_t qfp4_epilogue_backward_workspace_bytes(int64_t M, int64_t N)
 {
     if (M <= 0 || N <= 0 || M > INT32_MAX / 2 || N > INT32_MAX / 2) return 0;
-    return sizeof(float) * epilogue_chunks(M, N) * N;
+    size_t most = 0;
+    for (int V = 4; V <= 8; V += 4) {
+        const EbGrid g = epilogue_backward_grid(M, N, V);
+        most = imax(most, sizeof(float) * g.chunks * g.tiles * (EB_TILE * V + V));
+    }
+    return most;
 }
 
 extern "C" int qfp4_epilogue_backward(const void *dY, const void *Z, qfp4_dtype dt, int64_t M, int64_t N, qfp4_act act,
@@ -180,13 +296,8 @@ extern "C" int qfp4_epilogue_backward(const void *dY, const void *Z, qfp4_dtype 
         return QFP4_OK;
     }
     if (dbias && (!workspace || workspace_bytes < qfp4_epilogue_backward_workspace_bytes(M, N))) return QFP4_ERR_ARG;
-    const int64_t chunks = epilogue_chunks(M, N), rows = (M + chunks - 1) / chunks;
-    const int64_t used = (M + rows - 1) / rows;
-    float *partial = dbias ? static_cast<float *>(workspace) : nullptr;
-    const dim3 grid(static_cast<unsigned>((N + 255) / 256), static_cast<unsigned>(used));
     const DropParams d = drop_params(dropout_p, seed, step);
-    if (dt == QFP4_F32) k_epilogue_backward<QFP4_F32><<<grid, 256, 0, s>>>(dY, Z, M, N, rows, act, d, dZ, partial);
-    else k_epilogue_backward<QFP4_BF16><<<grid, 256, 0, s>>>(dY, Z, M, N, rows, act, d, dZ, partial);
-    QFP4_LAUNCH_CHECK();
-    return dbias ? column_sums(partial, used, N, dbias, nullptr, false, s) : QFP4_OK;
+    float *partial = static_cast<float *>(workspace);
+    return dt == QFP4_F32 ? epilogue_backward<QFP4_F32>(dY, Z, M, N, act, d, dZ, dbias, partial, s)
+                          : epilogue_backward<QFP4_BF16>(dY, Z, M, N, act, d, dZ, dbias, partial, s);
 }

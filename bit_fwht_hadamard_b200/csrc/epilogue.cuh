@@ -152,7 +152,7 @@ __device__ __forceinline__ void act_backward(float *d, const float *zin, int act
     switch (act) {
     case QFP4_ACT_RELU:
 #pragma unroll
-        for (int t = 0; t < N; ++t) d[t] = z[t] > 0.0f ? d[t] : z[t] <= 0.0f ? 0.0f : z[t];
+        for (int t = 0; t < N; ++t) d[t] = z[t] > 0.0f ? d[t] : 0.0f;
         break;
     case QFP4_ACT_GELU:
 #pragma unroll

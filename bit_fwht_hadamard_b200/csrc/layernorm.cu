@@ -5,60 +5,129 @@
 // xhat = (x - mean) rstd and g = dy gamma:
 //   dx = rstd (g - mean_d(g) - xhat mean_d(g xhat)),
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy.
-#include "epilogue.cuh"
+//
+// Bound by memory: each call reads its matrices once and writes its result
+// once.  A row lies in the registers of the group of threads that takes it
+// (a warp, or a block of 128 to 1024), in vectors of 16 bytes where the rows
+// start on 16 bytes and element by element where they do not, so the second
+// pass of the variance (on x - mean, which keeps a large mean from cancelling)
+// costs no second read.  Longer rows are read again from the caches.
+#include "vec.cuh"
 
 namespace qfp4 {
 
-// Sums of a and b over the block, in every thread; red: 64 floats.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float *red)
+template <int DT>
+__host__ __device__ constexpr int ln_v()
 {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    __syncthreads();
-    if (lane == 0) {
-        red[warp] = a;
-        red[32 + warp] = b;
-    }
-    __syncthreads();
-    a = lane < nw ? red[lane] : 0.0f;
-    b = lane < nw ? red[32 + lane] : 0.0f;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    }
-    return make_float2(a, b);
+    return DT == QFP4_F32 ? 4 : 8;
 }
 
-// A block a row; three reads of the row (the first from memory, the others
-// from the caches).
-template <int DT>
-__global__ void __launch_bounds__(256) k_layernorm(const void *x, int64_t M, int64_t D, const void *gamma,
-                                                    const void *beta, int w32, float eps, void *y, float *mean_out,
-                                                    float *rstd_out)
+// ------------------------------------------------------------------ forward
+// G threads a row, NV vectors of V elements each: D <= G NV V.
+template <int DT, int V, int G, int NV>
+__global__ void __launch_bounds__(G == 32 ? 128 : G)
+    k_layernorm(const void *x, int64_t M, int D, const void *gamma, const void *beta, int w32, float eps, void *y,
+                float *mean_out, float *rstd_out)
 {
-    __shared__ float red[64];
+    __shared__ float red[2][G == 32 ? 1 : G / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t m = G == 32 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x;
+    if (m >= M) return;                                       // a whole group
+    const int64_t r = m * D;
+    const int nv = D / V;
+    Vec<DT, V> raw[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (t + k * G < nv) raw[k].load(x, r + static_cast<int64_t>(t + k * G) * V);
+    const float inv = 1.0f / static_cast<float>(D);
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (t + k * G < nv) {
+            float v[V];
+            raw[k].get(v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s += v[j];
+        }
+    const float mean = group_sum<G>(s, red[0]) * inv;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (t + k * G < nv) {
+            float v[V];
+            raw[k].get(v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] -= mean;
+                s = fmaf(v[j], v[j], s);
+            }
+        }
+    const float rstd = 1.0f / sqrtf(group_sum<G>(s, red[1]) * inv + eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (t + k * G < nv) {
+            const int64_t c = static_cast<int64_t>(t + k * G) * V;
+            float v[V], w[V];
+            raw[k].get(v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = (v[j] - mean) * rstd;
+            if (gamma) {
+                ld_param<V>(gamma, w32, c, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] *= w[j];
+            }
+            if (beta) {
+                ld_param<V>(beta, w32, c, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] += w[j];
+            }
+            raw[k].set(v);
+            raw[k].store(y, r + c);
+        }
+    if (t == 0) {
+        if (mean_out) mean_out[m] = mean;
+        if (rstd_out) rstd_out[m] = rstd;
+    }
+}
+
+// Rows of any length: a block of 1024 a row, three reads of it.
+template <int DT>
+__global__ void __launch_bounds__(1024) k_layernorm_long(const void *x, int64_t M, int64_t D, const void *gamma,
+                                                          const void *beta, int w32, float eps, void *y,
+                                                          float *mean_out, float *rstd_out)
+{
+    __shared__ float red[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const float inv = 1.0f / static_cast<float>(D);
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
         const int64_t r = m * D;
-        float s = 0.0f;
-        for (int64_t c = threadIdx.x; c < D; c += blockDim.x) s += ld_as_float(x, DT == QFP4_F32, r + c);
-        const float mean = block_sum2(s, 0.0f, red).x / static_cast<float>(D);
-        s = 0.0f;
-        for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
-            const float t = ld_as_float(x, DT == QFP4_F32, r + c) - mean;
-            s += t * t;
-        }
-        const float rstd = 1.0f / sqrtf(block_sum2(s, 0.0f, red).x / static_cast<float>(D) + eps);
-        for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
+        // four sums a thread: D / 4096 terms one after the other
+        float s[4] = {};
+        for (int64_t c = threadIdx.x; c < D; c += 4096)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + 1024 * j < D) s[j] += ld_as_float(x, DT == QFP4_F32, r + c + 1024 * j);
+        const float mean = group_sum<1024>((s[0] + s[1]) + (s[2] + s[3]), red[0]) * inv;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = 0.0f;
+        for (int64_t c = threadIdx.x; c < D; c += 4096)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + 1024 * j < D) {
+                    const float t = ld_as_float(x, DT == QFP4_F32, r + c + 1024 * j) - mean;
+                    s[j] = fmaf(t, t, s[j]);
+                }
+        const float rstd = 1.0f / sqrtf(group_sum<1024>((s[0] + s[1]) + (s[2] + s[3]), red[1]) * inv + eps);
+        for (int64_t c = threadIdx.x; c < D; c += 1024) {
             float v = (ld_as_float(x, DT == QFP4_F32, r + c) - mean) * rstd;
             if (gamma) v *= ld_as_float(gamma, w32, c);
             if (beta) v += ld_as_float(beta, w32, c);
-            if (DT == QFP4_F32) static_cast<float *>(y)[r + c] = v;
-            else static_cast<__nv_bfloat16 *>(y)[r + c] = __float2bfloat16_rn(v);
+            Vec<DT, 1> o;
+            o.set(&v);
+            o.store(y, r + c);
         }
         if (threadIdx.x == 0) {
             if (mean_out) mean_out[m] = mean;
@@ -67,31 +136,214 @@ __global__ void __launch_bounds__(256) k_layernorm(const void *x, int64_t M, int
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256) k_layernorm_dx(const void *dy, const void *x, int64_t M, int64_t D,
-                                                       const void *gamma, int w32, const float *mean_in,
-                                                       const float *rstd_in, void *dx)
+struct LnForward {
+    const void *x;
+    int64_t M, D;
+    const void *gamma, *beta;
+    int w32;
+    float eps;
+    void *y;
+    float *mean, *rstd;
+    cudaStream_t s;
+};
+
+template <int DT, int V, int G, int NV>
+static int launch_layernorm(const LnForward &a)
 {
-    __shared__ float red[64];
-    for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
+    const unsigned grid = static_cast<unsigned>(G == 32 ? (a.M + 3) / 4 : a.M);
+    if (launch_pdl(k_layernorm<DT, V, G, NV>, dim3(grid), dim3(G == 32 ? 128 : G), 0, a.s, a.x, a.M,
+                   static_cast<int>(a.D), a.gamma, a.beta, a.w32, a.eps, a.y, a.mean, a.rstd) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
+}
+
+// The group of a row: a warp up to 128 vectors; else four vectors a thread,
+// which keeps the most bytes in flight an SM, or, with so few rows that each
+// has an SM to itself, as many threads as there are vectors: the row's own
+// latency is then all there is.
+template <int DT, int V>
+static int layernorm_by_size(const LnForward &a)
+{
+    const int64_t nv = a.D / V;
+    const bool few = a.M <= 2 * 148;
+    if (nv <= 32) return launch_layernorm<DT, V, 32, 1>(a);
+    if (nv <= 64 && !few) return launch_layernorm<DT, V, 32, 2>(a);
+    if (nv <= 128 && !few) return launch_layernorm<DT, V, 32, 4>(a);
+    if (few) {
+        if (nv <= 128) return launch_layernorm<DT, V, 128, 1>(a);
+        if (nv <= 512) return launch_layernorm<DT, V, 512, 1>(a);
+        if (nv <= 1024) return launch_layernorm<DT, V, 1024, 1>(a);
+    }
+    if (nv <= 512) return launch_layernorm<DT, V, 128, 4>(a);
+    if (nv <= 1024) return launch_layernorm<DT, V, 256, 4>(a);
+    if (nv <= 2048) return launch_layernorm<DT, V, 512, 4>(a);
+    return launch_layernorm<DT, V, 1024, 4>(a);
+}
+
+template <int DT>
+static int layernorm_forward(const LnForward &a)
+{
+    constexpr int V = ln_v<DT>();
+    if (a.D % V == 0 && a.D / V <= 4096) return layernorm_by_size<DT, V>(a);
+    if (a.D <= 4096) return layernorm_by_size<DT, 1>(a);
+    const int grid = static_cast<int>(imin<int64_t>(a.M, 16 * num_sms()));
+    if (launch_pdl(k_layernorm_long<DT>, dim3(grid), dim3(1024), 0, a.s, a.x, a.M, a.D, a.gamma, a.beta, a.w32, a.eps,
+                   a.y, a.mean, a.rstd) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
+}
+
+// ------------------------------------------------------------------ backward
+// One pass: a group of G threads takes a row of every gridDim.x-th group,
+// NV vectors a thread; the next row's loads are issued before the row sums of
+// the present one are joined.  A thread keeps the sums of dy xhat and dy of
+// its own columns in registers over all its rows; at the end each block
+// writes them as one row of the partial sums (the four warps of a block with
+// G = 32 joined first).
+template <int DT, int V, int G, int NV>
+__global__ void __launch_bounds__(G == 32 ? 128 : G)
+    k_layernorm_backward(const void *dy, const void *x, int64_t M, int D, const void *gamma, int w32,
+                         const float *mean_in, const float *rstd_in, void *dx, float *partial)
+{
+    __shared__ float2 red[2][G == 32 ? 1 : G / 32];
+    __shared__ float join[G == 32 ? 3 : 1][G == 32 ? 32 * NV * V : 1];
+    pdl_wait();
+    pdl_trigger();
+    const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x, wg = G == 32 ? threadIdx.x >> 5 : 0;
+    const int nv = D / V;
+    const float inv = 1.0f / static_cast<float>(D);
+    float sg[NV * V], sb[NV * V], w[NV * V];
+#pragma unroll
+    for (int k = 0; k < NV * V; ++k) {
+        sg[k] = sb[k] = 0.0f;
+        w[k] = 1.0f;
+    }
+    if (gamma)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) ld_param<V>(gamma, w32, static_cast<int64_t>(t + k * G) * V, w + k * V);
+    const int64_t groups = G == 32 ? gridDim.x * 4ll : gridDim.x;
+    int64_t m = G == 32 ? blockIdx.x * 4ll + wg : blockIdx.x;
+    Vec<DT, V> rd[NV], rx[NV];
+    float mean = 0.0f, rstd = 0.0f;
+    auto load = [&](int64_t row) {
+        mean = mean_in[row];
+        rstd = rstd_in[row];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) {
+                const int64_t i = row * D + static_cast<int64_t>(t + k * G) * V;
+                rd[k].load(dy, i);
+                rx[k].load(x, i);
+            }
+    };
+    if (m < M) load(m);
+    for (int par = 0; m < M; m += groups, par ^= 1) {
+        float xh[NV * V], g[NV * V], s1 = 0.0f, s2 = 0.0f;
+        const float rs = rstd;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (t + k * G < nv) {
+                float d[V];
+                rd[k].get(d);
+                rx[k].get(xh + k * V);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int e = k * V + j;
+                    xh[e] = (xh[e] - mean) * rstd;
+                    sg[e] = fmaf(d[j], xh[e], sg[e]);
+                    sb[e] += d[j];
+                    g[e] = d[j] * w[e];
+                    s1 += g[e];
+                    s2 = fmaf(g[e], xh[e], s2);
+                }
+            }
+        }
+        if (m + groups < M) load(m + groups);
+        if (!dx) continue;
+        const float2 c = group_sum2<G>(s1, s2, red[par]);
+        const float c1 = c.x * inv, c2 = c.y * inv;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) {
+                float v[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) v[j] = rs * (g[k * V + j] - fmaf(xh[k * V + j], c2, c1));
+                Vec<DT, V> o;
+                o.set(v);
+                o.store(dx, m * D + static_cast<int64_t>(t + k * G) * V);
+            }
+    }
+    if (!partial) return;
+    float *pg = partial + static_cast<int64_t>(blockIdx.x) * D;
+    float *pb = pg + static_cast<int64_t>(gridDim.x) * D;
+    if constexpr (G == 32) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float *v = half ? sb : sg;
+            __syncthreads();
+            if (wg > 0)
+#pragma unroll
+                for (int k = 0; k < NV * V; ++k) join[wg - 1][k * 32 + t] = v[k];
+            __syncthreads();
+            if (wg == 0)
+#pragma unroll
+                for (int k = 0; k < NV * V; ++k)
+                    v[k] = (v[k] + join[0][k * 32 + t]) + (join[1][k * 32 + t] + join[2][k * 32 + t]);
+        }
+        if (wg > 0) return;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (t + k * G < nv)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int64_t c = static_cast<int64_t>(t + k * G) * V + j;
+                pg[c] = sg[k * V + j];
+                pb[c] = sb[k * V + j];
+            }
+}
+
+// Rows too long for that: the column sums and dx in a kernel each.
+template <int DT>
+__global__ void __launch_bounds__(1024) k_layernorm_dx_long(const void *dy, const void *x, int64_t M, int64_t D,
+                                                             const void *gamma, int w32, const float *mean_in,
+                                                             const float *rstd_in, void *dx)
+{
+    __shared__ float2 red[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const float inv = 1.0f / static_cast<float>(D);
+    int par = 0;
+    for (int64_t m = blockIdx.x; m < M; m += gridDim.x, par ^= 1) {
         const int64_t r = m * D;
         const float mean = mean_in[m], rstd = rstd_in[m];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
+        float s1[4] = {}, s2[4] = {};
+        for (int64_t c = threadIdx.x; c < D; c += 4096)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + 1024 * j < D) {
+                    float g = ld_as_float(dy, DT == QFP4_F32, r + c + 1024 * j);
+                    if (gamma) g *= ld_as_float(gamma, w32, c + 1024 * j);
+                    s1[j] += g;
+                    s2[j] = fmaf(g, (ld_as_float(x, DT == QFP4_F32, r + c + 1024 * j) - mean) * rstd, s2[j]);
+                }
+        const float2 t = group_sum2<1024>((s1[0] + s1[1]) + (s1[2] + s1[3]), (s2[0] + s2[1]) + (s2[2] + s2[3]),
+                                          red[par]);
+        const float c1 = t.x * inv, c2 = t.y * inv;
+        for (int64_t c = threadIdx.x; c < D; c += 1024) {
             float g = ld_as_float(dy, DT == QFP4_F32, r + c);
             if (gamma) g *= ld_as_float(gamma, w32, c);
-            s1 += g;
-            s2 += g * ((ld_as_float(x, DT == QFP4_F32, r + c) - mean) * rstd);
-        }
-        const float2 t = block_sum2(s1, s2, red);
-        const float c1 = t.x / static_cast<float>(D), c2 = t.y / static_cast<float>(D);
-        for (int64_t c = threadIdx.x; c < D; c += blockDim.x) {
-            float g = ld_as_float(dy, DT == QFP4_F32, r + c);
-            if (gamma) g *= ld_as_float(gamma, w32, c);
-            const float xh = (ld_as_float(x, DT == QFP4_F32, r + c) - mean) * rstd;
-            const float v = rstd * (g - c1 - xh * c2);
-            if (DT == QFP4_F32) static_cast<float *>(dx)[r + c] = v;
-            else static_cast<__nv_bfloat16 *>(dx)[r + c] = __float2bfloat16_rn(v);
+            const float v = rstd * (g - fmaf((ld_as_float(x, DT == QFP4_F32, r + c) - mean) * rstd, c2, c1));
+            Vec<DT, 1> o;
+            o.set(&v);
+            o.store(dx, r + c);
         }
     }
 }
@@ -99,21 +351,131 @@ __global__ void __launch_bounds__(256) k_layernorm_dx(const void *dy, const void
 // Column sums of a chunk of rows: partial[0][chunk][D] of dy xhat,
 // partial[1][chunk][D] of dy.
 template <int DT>
-__global__ void __launch_bounds__(256) k_layernorm_dw(const void *dy, const void *x, int64_t M, int64_t D,
-                                                       int64_t rows, const float *mean, const float *rstd,
-                                                       float *partial)
+__global__ void __launch_bounds__(256) k_layernorm_dw_long(const void *dy, const void *x, int64_t M, int64_t D,
+                                                            int64_t rows, const float *mean, const float *rstd,
+                                                            float *partial)
 {
+    pdl_wait();
+    pdl_trigger();
     const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (c >= D) return;
     const int64_t m0 = blockIdx.y * rows, m1 = imin(M, m0 + rows);
     float sg = 0.0f, sb = 0.0f;
+#pragma unroll 4
     for (int64_t m = m0; m < m1; ++m) {
         const float d = ld_as_float(dy, DT == QFP4_F32, m * D + c);
-        sg += d * ((ld_as_float(x, DT == QFP4_F32, m * D + c) - mean[m]) * rstd[m]);
+        sg = fmaf(d, (ld_as_float(x, DT == QFP4_F32, m * D + c) - mean[m]) * rstd[m], sg);
         sb += d;
     }
     partial[blockIdx.y * D + c] = sg;
-    partial[(gridDim.y + blockIdx.y) * D + c] = sb;
+    partial[(static_cast<int64_t>(gridDim.y) + blockIdx.y) * D + c] = sb;
+}
+
+// How the backward pass runs: threads a row G and vectors a thread NV of the
+// one-pass kernel (G = 0: the kernels for long rows), and the rows of partial
+// sums that it writes.
+struct LnPlan {
+    int V, G, NV;
+    int64_t parts, rows;
+};
+
+static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
+{
+    LnPlan p{};
+    const int vec = f32 ? 4 : 8;
+    p.V = D % vec == 0 ? vec : 1;
+    const int64_t nv = D / p.V;
+    // element by element a thread holds up to four, else one vector (two of
+    // binary32) or, in a warp, up to two
+    if (nv <= 32) p.G = 32, p.NV = 1;
+    else if (nv <= 64) p.G = 32, p.NV = 2;
+    else if (nv <= 128) p.G = 128, p.NV = 1;
+    else if (nv <= 256) p.G = 256, p.NV = 1;
+    else if (nv <= 512) p.G = 512, p.NV = 1;
+    else if (nv <= 1024) p.G = 1024, p.NV = 1;
+    else if (nv <= 2048 && p.V < 8) p.G = 1024, p.NV = 2;
+    else if (nv <= 4096 && p.V == 1) p.G = 1024, p.NV = 4;
+    if (p.G) {
+        // blocks for 1024 threads an SM, but no more than there are rows
+        const int64_t per = p.G == 32 ? 4 : 1, threads = p.G == 32 ? 128 : p.G;
+        p.parts = imin<int64_t>((M + per - 1) / per, 148 * imax<int64_t>(1, 1024 / threads));
+    } else {
+        const int64_t cols = (D + 255) / 256;
+        const int64_t want = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));
+        p.rows = (M + want - 1) / want;
+        p.parts = (M + p.rows - 1) / p.rows;
+    }
+    return p;
+}
+
+struct LnBackward {
+    const void *dy, *x;
+    int64_t M, D;
+    const void *gamma;
+    int w32;
+    const float *mean, *rstd;
+    void *dx;
+    float *partial;
+    cudaStream_t s;
+};
+
+template <int DT, int V, int G, int NV>
+static int launch_layernorm_backward(const LnBackward &a, const LnPlan &p)
+{
+    if (launch_pdl(k_layernorm_backward<DT, V, G, NV>, dim3(static_cast<unsigned>(p.parts)),
+                   dim3(G == 32 ? 128 : G), 0, a.s, a.dy, a.x, a.M, static_cast<int>(a.D), a.gamma, a.w32, a.mean,
+                   a.rstd, a.dx, a.partial) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
+}
+
+template <int DT, int V>
+static int layernorm_backward_by_size(const LnBackward &a, const LnPlan &p)
+{
+    if (p.G == 32) return p.NV == 1 ? launch_layernorm_backward<DT, V, 32, 1>(a, p)
+                                    : launch_layernorm_backward<DT, V, 32, 2>(a, p);
+    if (p.G == 128) return launch_layernorm_backward<DT, V, 128, 1>(a, p);
+    if (p.G == 256) return launch_layernorm_backward<DT, V, 256, 1>(a, p);
+    if (p.G == 512) return launch_layernorm_backward<DT, V, 512, 1>(a, p);
+    if constexpr (V < 8)
+        if (p.NV == 2) return launch_layernorm_backward<DT, V, 1024, 2>(a, p);
+    if constexpr (V == 1)
+        if (p.NV == 4) return launch_layernorm_backward<DT, V, 1024, 4>(a, p);
+    return launch_layernorm_backward<DT, V, 1024, 1>(a, p);
+}
+
+template <int DT>
+static int layernorm_backward(const LnBackward &a, const LnPlan &p, float *dgamma, float *dbeta)
+{
+    if (p.G) {
+        const int st = p.V == 1 ? layernorm_backward_by_size<DT, 1>(a, p)
+                                : layernorm_backward_by_size<DT, ln_v<DT>()>(a, p);
+        if (st != QFP4_OK || !a.partial) return st;
+        return column_sums(a.partial, p.parts, a.D, static_cast<int>(a.D), 0, 1, dgamma, dbeta, true, a.s);
+    }
+    if (a.partial) {                                          // first: dx may overwrite dy
+        const dim3 grid(static_cast<unsigned>((a.D + 255) / 256), static_cast<unsigned>(p.parts));
+        if (launch_pdl(k_layernorm_dw_long<DT>, grid, dim3(256), 0, a.s, a.dy, a.x, a.M, a.D, p.rows, a.mean, a.rstd,
+                       a.partial) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return QFP4_ERR_CUDA;
+        }
+        QFP4_LAUNCH_CHECK();
+        const int st = column_sums(a.partial, p.parts, a.D, static_cast<int>(a.D), 0, 1, dgamma, dbeta, true, a.s);
+        if (st != QFP4_OK) return st;
+    }
+    if (!a.dx) return QFP4_OK;
+    const int grid = static_cast<int>(imin<int64_t>(a.M, 16 * num_sms()));
+    if (launch_pdl(k_layernorm_dx_long<DT>, dim3(grid), dim3(1024), 0, a.s, a.dy, a.x, a.M, a.D, a.gamma, a.w32, a.mean,
+                   a.rstd, a.dx) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
 }
 
 }  // namespace qfp4
@@ -140,18 +502,16 @@ extern "C" int qfp4_layernorm_forward(const void *x, qfp4_dtype dt, int64_t M, i
         return QFP4_ERR_ALIGN;
     if (M == 0) return QFP4_OK;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int grid = static_cast<int>(imin<int64_t>(M, 64 * num_sms()));
-    const int w32 = wdt == QFP4_F32;
-    if (dt == QFP4_F32) k_layernorm<QFP4_F32><<<grid, 256, 0, s>>>(x, M, D, gamma, beta, w32, eps, y, mean, rstd);
-    else k_layernorm<QFP4_BF16><<<grid, 256, 0, s>>>(x, M, D, gamma, beta, w32, eps, y, mean, rstd);
-    QFP4_LAUNCH_CHECK();
-    return QFP4_OK;
+    const LnForward a{x, M, D, gamma, beta, wdt == QFP4_F32, eps, y, mean, rstd, s};
+    return dt == QFP4_F32 ? layernorm_forward<QFP4_F32>(a) : layernorm_forward<QFP4_BF16>(a);
 }
 
 extern "C" size_t qfp4_layernorm_backward_workspace_bytes(int64_t M, int64_t D)
 {
     if (M <= 0 || D <= 0 || layernorm_shape(M, D) != QFP4_OK) return 0;
-    return 2 * sizeof(float) * epilogue_chunks(M, D) * D;
+    // of either type
+    const int64_t parts = imax(layernorm_backward_plan(M, D, false).parts, layernorm_backward_plan(M, D, true).parts);
+    return 2 * sizeof(float) * parts * D;
 }
 
 extern "C" int qfp4_layernorm_backward(const void *dy, const void *x, qfp4_dtype dt, int64_t M, int64_t D,
@@ -175,23 +535,9 @@ extern "C" int qfp4_layernorm_backward(const void *dy, const void *x, qfp4_dtype
     }
     const bool dw = dgamma || dbeta;
     if (dw && (!workspace || workspace_bytes < qfp4_layernorm_backward_workspace_bytes(M, D))) return QFP4_ERR_ARG;
-    // dgamma and dbeta first: dx may overwrite dy
-    if (dw) {
-        const int64_t chunks = epilogue_chunks(M, D), rows = (M + chunks - 1) / chunks, used = (M + rows - 1) / rows;
-        float *partial = static_cast<float *>(workspace);
-        const dim3 grid(static_cast<unsigned>((D + 255) / 256), static_cast<unsigned>(used));
-        if (dt == QFP4_F32) k_layernorm_dw<QFP4_F32><<<grid, 256, 0, s>>>(dy, x, M, D, rows, mean, rstd, partial);
-        else k_layernorm_dw<QFP4_BF16><<<grid, 256, 0, s>>>(dy, x, M, D, rows, mean, rstd, partial);
-        QFP4_LAUNCH_CHECK();
-        const int st = column_sums(partial, used, D, dgamma, dbeta, true, s);
-        if (st != QFP4_OK) return st;
-    }
-    const int w32 = wdt == QFP4_F32;
-    if (dx) {
-        const int grid = static_cast<int>(imin<int64_t>(M, 64 * num_sms()));
-        if (dt == QFP4_F32) k_layernorm_dx<QFP4_F32><<<grid, 256, 0, s>>>(dy, x, M, D, gamma, w32, mean, rstd, dx);
-        else k_layernorm_dx<QFP4_BF16><<<grid, 256, 0, s>>>(dy, x, M, D, gamma, w32, mean, rstd, dx);
-        QFP4_LAUNCH_CHECK();
-    }
-    return QFP4_OK;
+    const LnBackward a{dy, x, M, D, gamma, wdt == QFP4_F32, mean, rstd, dx,
+                       dw ? static_cast<float *>(workspace) : nullptr, s};
+    const LnPlan p = layernorm_backward_plan(M, D, dt == QFP4_F32);
+    return dt == QFP4_F32 ? layernorm_backward<QFP4_F32>(a, p, dgamma, dbeta)
+                          : layernorm_backward<QFP4_BF16>(a, p, dgamma, dbeta);
 }

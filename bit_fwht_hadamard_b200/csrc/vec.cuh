@@ -1,0 +1,146 @@
+// vec.cuh -- sixteen-byte vectors of bf16 or binary32 values, and reductions,
+// for the elementwise and row kernels (dropout, epilogue backward, layer norm).
+#pragma once
+
+#include "epilogue.cuh"
+
+namespace qfp4 {
+
+// V values of type DT at element i: 16 bytes (V = 8 bf16 or 4 binary32; i a
+// multiple of V), or one value (V = 1).  Raw holds them as loaded.
+template <int DT, int V>
+struct Vec {
+    static constexpr int W = V * (DT == QFP4_F32 ? 4 : 2) / 4;   // 32-bit words
+    static_assert(V == 1 || W == 4, "16 bytes or one value");
+    uint32_t r[V == 1 ? 1 : 4];
+
+    __device__ __forceinline__ void load(const void *p, int64_t i)
+    {
+        if constexpr (V > 1) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + i * (DT == QFP4_F32 ? 4 : 2));
+            r[0] = u.x;
+            r[1] = u.y;
+            r[2] = u.z;
+            r[3] = u.w;
+        } else if constexpr (DT == QFP4_F32)
+            r[0] = static_cast<const uint32_t *>(p)[i];
+        else
+            r[0] = static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]);
+    }
+    __device__ __forceinline__ void get(float *v) const
+    {
+#pragma unroll
+        for (int t = 0; t < V; ++t) {
+            if constexpr (DT == QFP4_F32) v[t] = __uint_as_float(r[t]);
+            else v[t] = t & 1 ? bf16hi(r[t >> 1]) : bf16lo(r[t >> 1]);
+        }
+    }
+    // one rounding to DT
+    __device__ __forceinline__ void set(const float *v)
+    {
+        if constexpr (DT == QFP4_F32) {
+#pragma unroll
+            for (int t = 0; t < V; ++t) r[t] = __float_as_uint(v[t]);
+        } else if constexpr (V == 1)
+            r[0] = pack_bf16(v[0], 0.0f);
+        else {
+#pragma unroll
+            for (int t = 0; t < V; t += 2) r[t >> 1] = pack_bf16(v[t], v[t + 1]);
+        }
+    }
+    __device__ __forceinline__ void store(void *p, int64_t i) const
+    {
+        if constexpr (V > 1)
+            *reinterpret_cast<uint4 *>(static_cast<char *>(p) + i * (DT == QFP4_F32 ? 4 : 2)) =
+                make_uint4(r[0], r[1], r[2], r[3]);
+        else if constexpr (DT == QFP4_F32)
+            static_cast<uint32_t *>(p)[i] = r[0];
+        else
+            static_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(r[0]);
+    }
+    // element t alone (of the vector that starts at element i of p)
+    __device__ __forceinline__ void load1(const void *p, int64_t i, int t)
+    {
+        if constexpr (DT == QFP4_F32) r[t] = static_cast<const uint32_t *>(p)[i + t];
+        else {
+            const uint32_t h = static_cast<const uint16_t *>(p)[i + t];
+            r[t >> 1] = t & 1 ? (r[t >> 1] & 0xFFFFu) | (h << 16) : (r[t >> 1] & 0xFFFF0000u) | h;
+        }
+    }
+    __device__ __forceinline__ void store1(void *p, int64_t i, int t) const
+    {
+        if constexpr (DT == QFP4_F32) static_cast<uint32_t *>(p)[i + t] = r[t];
+        else static_cast<uint16_t *>(p)[i + t] = static_cast<uint16_t>(t & 1 ? r[t >> 1] >> 16 : r[t >> 1]);
+    }
+};
+
+// V parameter values (gamma, beta) from column c on (c a multiple of V), of
+// either type.
+template <int V>
+__device__ __forceinline__ void ld_param(const void *p, int f32, int64_t c, float *v)
+{
+    if constexpr (V == 1) v[0] = ld_as_float(p, f32, c);
+    else if (f32) {
+#pragma unroll
+        for (int t = 0; t < V; t += 4) {
+            const float4 u = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c + t));
+            v[t] = u.x;
+            v[t + 1] = u.y;
+            v[t + 2] = u.z;
+            v[t + 3] = u.w;
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < V; t += 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + c + t));
+            v[t] = bf16lo(u.x);
+            v[t + 1] = bf16hi(u.x);
+            v[t + 2] = bf16lo(u.y);
+            v[t + 3] = bf16hi(u.y);
+        }
+    }
+}
+
+__device__ __forceinline__ float warp_sum(float a)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+    return a;
+}
+
+// Sum of G threads' values in each of them (G = 32: the warp; else the whole
+// block of G), in a fixed order.  red: G / 32 floats that nothing else uses
+// until the block's next barrier after this one.
+template <int G>
+__device__ __forceinline__ float group_sum(float a, float *red)
+{
+    a = warp_sum(a);
+    if constexpr (G > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+        __syncthreads();
+        a = 0.0f;
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w) a += red[w];
+    }
+    return a;
+}
+template <int G>
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *red)
+{
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if constexpr (G > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.0f;
+#pragma unroll
+        for (int w = 0; w < G / 32; ++w) {
+            const float2 t = red[w];
+            a += t.x;
+            b += t.y;
+        }
+    }
+    return make_float2(a, b);
+}
+
+}  // namespace qfp4
