@@ -172,9 +172,7 @@ __global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const
     const bool full = c0 >= 0 && c0 + V <= N, some = c0 + V > 0 && c0 < N;
     const int64_t m0 = blockIdx.y * rows, m1 = imin(M, m0 + rows);
     const bool use_z = act != QFP4_ACT_NONE;
-    float sum[V];
-#pragma unroll
-    for (int t = 0; t < V; ++t) sum[t] = 0.0f;
+    Fv<V> sums = Fv<V>::splat(0.0f);
     for (int64_t m = m0 + w; m < m1; m += 8 * U) {
         Vec<DT, V> g[U], a[U];
 #pragma unroll
@@ -207,8 +205,7 @@ __global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const
                 a[u].get(x);
                 act_backward<V>(v, x, act);
             }
-#pragma unroll
-            for (int t = 0; t < V; ++t) sum[t] += v[t];         // zero outside the row
+            sums = sums + Fv<V>::of(v);                         // zero outside the row
             g[u].set(v);
             if (full) g[u].store(dz, i);
             else {
@@ -222,6 +219,8 @@ __global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const
     // slot V + j of red: column blockIdx.x TW + j; a warp covers j = -off .. TW - off - 1
     for (int j = lane; j < V; j += 32) red[w][j] = red[w][TW + j] = 0.0f;
     __syncwarp();
+    float sum[V];
+    sums.to(sum);
 #pragma unroll
     for (int t = 0; t < V; ++t) red[w][V + lane * V + t - off] = sum[t];
     __syncthreads();

@@ -102,6 +102,45 @@ __device__ __forceinline__ uint64_t phi2(uint64_t z)
     return f2pack(__saturatef(fmaf(a, qa, 0.5f)), __saturatef(fmaf(b, qb, 0.5f)));
 }
 
+// x within [-most, most]; a NaN stays one.
+__device__ __forceinline__ float clamp_nan(float x, float most)
+{
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}"
+        : "=f"(r)
+        : "f"(x), "f"(most), "f"(-most));
+    return r;
+}
+// GELU's slope Phi(z) + z phi(z) of a pair: again 1/2 plus an odd entire
+// function, with a polynomial of degree 17 in u = z^2 / 18 - 1 for |z| <= 6;
+// beyond that it is 0 or 1 to 4e-8.  Error below 2.5e-7.  A NaN stays one.
+__device__ __forceinline__ uint64_t gelu_slope2(uint64_t z)
+{
+    float a, b;
+    f2unpack(z, a, b);
+    const uint64_t c = f2pack(clamp_nan(a, 6.0f), clamp_nan(b, 6.0f));
+    const uint64_t u = f2fma(f2mul(c, c), f2pack(0.055555556f, 0.055555556f), f2pack(-1.0f, -1.0f));
+    uint64_t q = f2pack(-0.00594642246f, -0.00594642246f);
+    q = f2fma(q, u, f2pack(0.0139311319f, 0.0139311319f));
+    q = f2fma(q, u, f2pack(-0.00219016708f, -0.00219016708f));
+    q = f2fma(q, u, f2pack(-0.00573054375f, -0.00573054375f));
+    q = f2fma(q, u, f2pack(-0.026627304f, -0.026627304f));
+    q = f2fma(q, u, f2pack(0.0525551736f, 0.0525551736f));
+    q = f2fma(q, u, f2pack(-0.041894719f, -0.041894719f));
+    q = f2fma(q, u, f2pack(0.0424954034f, 0.0424954034f));
+    q = f2fma(q, u, f2pack(-0.0629948974f, -0.0629948974f));
+    q = f2fma(q, u, f2pack(0.0708191022f, 0.0708191022f));
+    q = f2fma(q, u, f2pack(-0.0650838539f, -0.0650838539f));
+    q = f2fma(q, u, f2pack(0.0579622947f, 0.0579622947f));
+    q = f2fma(q, u, f2pack(-0.0508224741f, -0.0508224741f));
+    q = f2fma(q, u, f2pack(0.04462317f, 0.04462317f));
+    q = f2fma(q, u, f2pack(-0.0423730016f, -0.0423730016f));
+    q = f2fma(q, u, f2pack(0.0460553207f, 0.0460553207f));
+    q = f2fma(q, u, f2pack(-0.0593426675f, -0.0593426675f));
+    q = f2fma(q, u, f2pack(0.117897779f, 0.117897779f));
+    return f2fma(c, q, f2pack(0.5f, 0.5f));
+}
+
 // 1 / (1 + e^-x); 0 for x -> -inf (the fast division gives 0 for a huge
 // divisor), 1 for x -> inf.
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
@@ -140,15 +179,10 @@ __device__ __forceinline__ void act_forward(float *v, int act)
     }
 }
 
-// d[t] *= act'(z[t]).  Beyond |z| = 80 every slope is 0 or 1 to binary32; the
-// clamp keeps z^2, z^3 and their products finite there.
+// d[t] *= act'(z[t]) on N values (N even).
 template <int N>
-__device__ __forceinline__ void act_backward(float *d, const float *zin, int act)
+__device__ __forceinline__ void act_backward(float *d, const float *z, int act)
 {
-    if (act == QFP4_ACT_NONE) return;
-    float z[N];
-#pragma unroll
-    for (int t = 0; t < N; ++t) z[t] = zin[t] > 80.0f ? 80.0f : zin[t] < -80.0f ? -80.0f : zin[t];
     switch (act) {
     case QFP4_ACT_RELU:
 #pragma unroll
@@ -156,30 +190,25 @@ __device__ __forceinline__ void act_backward(float *d, const float *zin, int act
         break;
     case QFP4_ACT_GELU:
 #pragma unroll
-        for (int t = 0; t < N; t += 2) {
-            float p[2];
-            f2unpack(phi2(f2pack(z[t], z[t + 1])), p[0], p[1]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float x = z[t + k];
-                d[t + k] *= fmaf(x * 0.3989422804f, __expf(-0.5f * x * x), p[k]);
-            }
-        }
+        for (int t = 0; t < N; t += 2)
+            f2unpack(f2mul(f2pack(d[t], d[t + 1]), gelu_slope2(f2pack(z[t], z[t + 1]))), d[t], d[t + 1]);
         break;
     case QFP4_ACT_GELU_TANH:
+        // beyond |z| = 80 the slope is 0 or 1 to binary32; the clamp keeps z^3 and the products finite
 #pragma unroll
         for (int t = 0; t < N; ++t) {
-            const float x = z[t], f = sigmoid_fast(gelu_tanh_arg(x));
+            const float x = clamp_nan(z[t], 80.0f), f = sigmoid_fast(gelu_tanh_arg(x));
             d[t] *= fmaf(x * f * (1.0f - f), fmaf(0.214064448f * x, x, 1.5957691216f), f);
         }
         break;
-    default:                                            // SiLU
+    case QFP4_ACT_SILU:
 #pragma unroll
         for (int t = 0; t < N; ++t) {
             const float f = sigmoid_fast(z[t]);
             d[t] *= f * fmaf(z[t], 1.0f - f, 1.0f);
         }
         break;
+    default: break;
     }
 }
 

@@ -42,48 +42,33 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
     for (int k = 0; k < NV; ++k)
         if (t + k * G < nv) raw[k].load(x, r + static_cast<int64_t>(t + k * G) * V);
     const float inv = 1.0f / static_cast<float>(D);
-    float s = 0.0f;
+    Fv<V> v[NV], s = Fv<V>::splat(0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         if (t + k * G < nv) {
-            float v[V];
-            raw[k].get(v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) s += v[j];
+            v[k] = raw[k].values();
+            s = s + v[k];
         }
-    const float mean = group_sum<G>(s, red[0]) * inv;
-    s = 0.0f;
+    const float mean = group_sum<G>(s.sum(), red[0]) * inv;
+    const Fv<V> mean2 = Fv<V>::splat(mean);
+    s = Fv<V>::splat(0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         if (t + k * G < nv) {
-            float v[V];
-            raw[k].get(v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] -= mean;
-                s = fmaf(v[j], v[j], s);
-            }
+            v[k] = v[k] - mean2;
+            s = fma(v[k], v[k], s);
         }
-    const float rstd = 1.0f / sqrtf(group_sum<G>(s, red[1]) * inv + eps);
+    const float rstd = 1.0f / sqrtf(group_sum<G>(s.sum(), red[1]) * inv + eps);
+    const Fv<V> rstd2 = Fv<V>::splat(rstd);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         if (t + k * G < nv) {
             const int64_t c = static_cast<int64_t>(t + k * G) * V;
-            float v[V], w[V];
-            raw[k].get(v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = (v[j] - mean) * rstd;
-            if (gamma) {
-                ld_param<V>(gamma, w32, c, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] *= w[j];
-            }
-            if (beta) {
-                ld_param<V>(beta, w32, c, w);
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] += w[j];
-            }
-            raw[k].set(v);
+            Fv<V> o = v[k] * rstd2;
+            if (gamma && beta) o = fma(o, ld_param<V>(gamma, w32, c), ld_param<V>(beta, w32, c));
+            else if (gamma) o = o * ld_param<V>(gamma, w32, c);
+            else if (beta) o = o + ld_param<V>(beta, w32, c);
+            raw[k].set(o);
             raw[k].store(y, r + c);
         }
     if (t == 0) {
@@ -218,16 +203,13 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
     const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x, wg = G == 32 ? threadIdx.x >> 5 : 0;
     const int nv = D / V;
     const float inv = 1.0f / static_cast<float>(D);
-    float sg[NV * V], sb[NV * V], w[NV * V];
+    Fv<V> sg[NV], sb[NV], w[NV];
 #pragma unroll
-    for (int k = 0; k < NV * V; ++k) {
-        sg[k] = sb[k] = 0.0f;
-        w[k] = 1.0f;
+    for (int k = 0; k < NV; ++k) {
+        sg[k] = sb[k] = Fv<V>::splat(0.0f);
+        w[k] = Fv<V>::splat(1.0f);
+        if (gamma && t + k * G < nv) w[k] = ld_param<V>(gamma, w32, static_cast<int64_t>(t + k * G) * V);
     }
-    if (gamma)
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (t + k * G < nv) ld_param<V>(gamma, w32, static_cast<int64_t>(t + k * G) * V, w + k * V);
     const int64_t groups = G == 32 ? gridDim.x * 4ll : gridDim.x;
     int64_t m = G == 32 ? blockIdx.x * 4ll + wg : blockIdx.x;
     Vec<DT, V> rd[NV], rx[NV];
@@ -245,48 +227,45 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
     };
     if (m < M) load(m);
     for (int par = 0; m < M; m += groups, par ^= 1) {
-        float xh[NV * V], g[NV * V], s1 = 0.0f, s2 = 0.0f;
-        const float rs = rstd;
+        Fv<V> xh[NV], g[NV], s1 = Fv<V>::splat(0.0f), s2 = Fv<V>::splat(0.0f);
+        const Fv<V> mean2 = Fv<V>::splat(mean), rstd2 = Fv<V>::splat(rstd);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (t + k * G < nv) {
-                float d[V];
-                rd[k].get(d);
-                rx[k].get(xh + k * V);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int e = k * V + j;
-                    xh[e] = (xh[e] - mean) * rstd;
-                    sg[e] = fmaf(d[j], xh[e], sg[e]);
-                    sb[e] += d[j];
-                    g[e] = d[j] * w[e];
-                    s1 += g[e];
-                    s2 = fmaf(g[e], xh[e], s2);
-                }
+                const Fv<V> d = rd[k].values();
+                xh[k] = (rx[k].values() - mean2) * rstd2;
+                sg[k] = fma(d, xh[k], sg[k]);
+                sb[k] = sb[k] + d;
+                g[k] = d * w[k];
+                s1 = s1 + g[k];
+                s2 = fma(g[k], xh[k], s2);
             }
         }
         if (m + groups < M) load(m + groups);
         if (!dx) continue;
-        const float2 c = group_sum2<G>(s1, s2, red[par]);
-        const float c1 = c.x * inv, c2 = c.y * inv;
+        const float2 c = group_sum2<G>(s1.sum(), s2.sum(), red[par], 1);
+        const Fv<V> c1 = Fv<V>::splat(c.x * inv), c2 = Fv<V>::splat(c.y * inv);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (t + k * G < nv) {
-                float v[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = rs * (g[k * V + j] - fmaf(xh[k * V + j], c2, c1));
                 Vec<DT, V> o;
-                o.set(v);
+                o.set(rstd2 * (g[k] - fma(xh[k], c2, c1)));
                 o.store(dx, m * D + static_cast<int64_t>(t + k * G) * V);
             }
     }
     if (!partial) return;
     float *pg = partial + static_cast<int64_t>(blockIdx.x) * D;
     float *pb = pg + static_cast<int64_t>(gridDim.x) * D;
+    float vg[NV * V], vb[NV * V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        sg[k].to(vg + k * V);
+        sb[k].to(vb + k * V);
+    }
     if constexpr (G == 32) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            float *v = half ? sb : sg;
+            float *v = half ? vb : vg;
             __syncthreads();
             if (wg > 0)
 #pragma unroll
@@ -305,9 +284,161 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int64_t c = static_cast<int64_t>(t + k * G) * V + j;
-                pg[c] = sg[k * V + j];
-                pb[c] = sb[k * V + j];
+                pg[c] = vg[k * V + j];
+                pb[c] = vb[k * V + j];
             }
+}
+
+// Aligned rows of 65 to 2048 vectors (bf16 D in (512, 16384], binary32 D in
+// (256, 8192]): the same pass with the rows of dy and x brought into shared
+// memory by bulk copies, `stages` rows ahead, so that no register waits for
+// memory.  One block an SM of GR groups of G threads, each group with rows, a
+// ring and a named barrier of its own; a thread holds NV vectors' columns.
+// The groups' sums are joined at the end, so there are no more partial rows
+// than SMs.  KEEP: xhat and g stay in registers between the row sums and dx;
+// else (1024 threads, 64 registers) they are formed again from shared memory.
+template <int DT, int G, int NV, int GR, bool KEEP>
+__global__ void __launch_bounds__(GR *G, 1)
+    k_layernorm_backward_ring(const void *dy, const void *x, int64_t M, int D, const void *gamma, int w32,
+                              const float *mean_in, const float *rstd_in, void *dx, float *partial, int stages)
+{
+    constexpr int V = ln_v<DT>(), ESZ = 16 / V, MAX_STAGES = 8;
+    extern __shared__ __align__(128) uint8_t ln_smem[];
+    __shared__ __align__(8) uint64_t full_sh[GR][MAX_STAGES];
+    __shared__ float2 red_sh[GR][2][G / 32];
+    const int t = threadIdx.x % G, gi = threadIdx.x / G, nv = D / V;
+    const int row_bytes = D * ESZ;
+    uint64_t *full = full_sh[gi];
+    uint8_t *ring = ln_smem + static_cast<size_t>(gi) * stages * 2 * row_bytes;
+    if (t == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const float inv = 1.0f / static_cast<float>(D);
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * GR, m0 = blockIdx.x * static_cast<int64_t>(GR) + gi;
+    // row number it of this group into its stage
+    auto issue = [&](int64_t it) {
+        const int64_t row = m0 + it * groups;
+        if (row >= M) return;
+        const int s = static_cast<int>(it % stages);
+        mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
+        bulk_g2s(ring + static_cast<size_t>(2 * s) * row_bytes, static_cast<const char *>(dy) + row * row_bytes, row_bytes,
+                 &full[s]);
+        bulk_g2s(ring + static_cast<size_t>(2 * s + 1) * row_bytes, static_cast<const char *>(x) + row * row_bytes, row_bytes,
+                 &full[s]);
+    };
+    if (t == 0)
+        for (int i = 0; i < stages - 1; ++i) issue(i);
+    Fv<V> sg[NV], sb[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) sg[k] = sb[k] = Fv<V>::splat(0.0f);
+    bool ok = true;
+    int64_t it = 0;
+    for (int64_t m = m0; m < M; m += groups, ++it) {
+        const int s = static_cast<int>(it % stages);
+        const float mean = mean_in[m], rstd = rstd_in[m];
+        if (!mbar_wait(&full[s], static_cast<uint32_t>(it / stages) & 1u)) {
+            ok = false;
+            break;
+        }
+        const uint8_t *pd = ring + static_cast<size_t>(2 * s) * row_bytes, *px = pd + row_bytes;
+        Fv<V> xh[KEEP ? NV : 1], g[KEEP ? NV : 1], s1 = Fv<V>::splat(0.0f), s2 = Fv<V>::splat(0.0f);
+        const Fv<V> mean2 = Fv<V>::splat(mean), rstd2 = Fv<V>::splat(rstd);
+        auto row_terms = [&](int c, Fv<V> &d, Fv<V> &h, Fv<V> &w) {
+            Vec<DT, V> a, b;
+            a.load(pd, c);
+            b.load(px, c);
+            d = a.values();
+            h = (b.values() - mean2) * rstd2;
+            w = gamma ? d * ld_param<V>(gamma, w32, c) : d;
+        };
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) {
+                Fv<V> d, &h = xh[KEEP ? k : 0], &w = g[KEEP ? k : 0];
+                row_terms((t + k * G) * V, d, h, w);
+                sg[k] = fma(d, h, sg[k]);
+                sb[k] = sb[k] + d;
+                s1 = s1 + w;
+                s2 = fma(w, h, s2);
+            }
+        // this thread's reads of the stages so far come before the next bulk copy
+        fence_proxy_async();
+        const float2 c = group_sum2<G>(s1.sum(), s2.sum(), red_sh[gi][it & 1], 1 + gi);
+        // every thread of the group is done with row it - 1, whose stage row
+        // it + stages - 1 takes
+        if (t == 0) issue(it + stages - 1);
+        if (!dx) continue;
+        const Fv<V> c1 = Fv<V>::splat(c.x * inv), c2 = Fv<V>::splat(c.y * inv);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) {
+                Fv<V> d, &h = xh[KEEP ? k : 0], &w = g[KEEP ? k : 0];
+                if constexpr (!KEEP) row_terms((t + k * G) * V, d, h, w);
+                Vec<DT, V> o;
+                o.set(rstd2 * (w - fma(h, c2, c1)));
+                o.store(dx, m * D + static_cast<int64_t>(t + k * G) * V);
+            }
+    }
+    if (!ok) settle_ns(kSettleNs);                            // copies already issued may still be landing
+    __syncthreads();
+    if (!partial) return;
+    // the other groups' sums, one group after the other, through shared memory
+    // (no copy is under way now) to the first
+    float *join = reinterpret_cast<float *>(ln_smem);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        Fv<V> *v = half ? sb : sg;
+#pragma unroll
+        for (int from = 1; from < GR; ++from) {
+            if (gi == from) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (t + k * G < nv) {
+                        float o[V];
+                        v[k].to(o);
+#pragma unroll
+                        for (int j = 0; j < V; j += 4)
+                            *reinterpret_cast<float4 *>(join + (t + k * G) * V + j) =
+                                make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
+            }
+            __syncthreads();
+            if (gi == 0) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (t + k * G < nv) {
+                        float o[V];
+#pragma unroll
+                        for (int j = 0; j < V; j += 4) {
+                            const float4 u = *reinterpret_cast<const float4 *>(join + (t + k * G) * V + j);
+                            o[j] = u.x;
+                            o[j + 1] = u.y;
+                            o[j + 2] = u.z;
+                            o[j + 3] = u.w;
+                        }
+                        v[k] = v[k] + Fv<V>::of(o);
+                    }
+            }
+            __syncthreads();
+        }
+        if (gi == 0) {
+            float *dst = partial + (half * static_cast<int64_t>(gridDim.x) + blockIdx.x) * D;
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (t + k * G < nv) {
+                    float o[V];
+                    v[k].to(o);
+#pragma unroll
+                    for (int j = 0; j < V; j += 4)
+                        *reinterpret_cast<float4 *>(dst + (t + k * G) * V + j) =
+                            make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+        }
+    }
 }
 
 // Rows too long for that: the column sums and dx in a kernel each.
@@ -335,7 +466,7 @@ __global__ void __launch_bounds__(1024) k_layernorm_dx_long(const void *dy, cons
                     s2[j] = fmaf(g, (ld_as_float(x, DT == QFP4_F32, r + c + 1024 * j) - mean) * rstd, s2[j]);
                 }
         const float2 t = group_sum2<1024>((s1[0] + s1[1]) + (s1[2] + s1[3]), (s2[0] + s2[1]) + (s2[2] + s2[3]),
-                                          red[par]);
+                                          red[par], 1);
         const float c1 = t.x * inv, c2 = t.y * inv;
         for (int64_t c = threadIdx.x; c < D; c += 1024) {
             float g = ld_as_float(dy, DT == QFP4_F32, r + c);
@@ -372,12 +503,13 @@ __global__ void __launch_bounds__(256) k_layernorm_dw_long(const void *dy, const
 }
 
 // How the backward pass runs: threads a row G and vectors a thread NV of the
-// one-pass kernel (G = 0: the kernels for long rows), and the rows of partial
-// sums that it writes.
+// one-pass kernels (G = 0: the kernels for long rows), `stages` of the ring
+// (0: rows in registers), and the rows of partial sums that it writes.
 struct LnPlan {
-    int V, G, NV;
+    int V, G, NV, GR, stages;
     int64_t parts, rows;
 };
+constexpr int LNB_SMEM = 200 * 1024;
 
 static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
 {
@@ -385,17 +517,28 @@ static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
     const int vec = f32 ? 4 : 8;
     p.V = D % vec == 0 ? vec : 1;
     const int64_t nv = D / p.V;
-    // element by element a thread holds up to four, else one vector (two of
-    // binary32) or, in a warp, up to two
     if (nv <= 32) p.G = 32, p.NV = 1;
     else if (nv <= 64) p.G = 32, p.NV = 2;
-    else if (nv <= 128) p.G = 128, p.NV = 1;
-    else if (nv <= 256) p.G = 256, p.NV = 1;
-    else if (nv <= 512) p.G = 512, p.NV = 1;
-    else if (nv <= 1024) p.G = 1024, p.NV = 1;
-    else if (nv <= 2048 && p.V < 8) p.G = 1024, p.NV = 2;
-    else if (nv <= 4096 && p.V == 1) p.G = 1024, p.NV = 4;
-    if (p.G) {
+    else if (p.V == 1) {
+        if (nv <= 128) p.G = 128, p.NV = 1;
+        else if (nv <= 512) p.G = 512, p.NV = 1;
+        else if (nv <= 1024) p.G = 1024, p.NV = 1;
+        else if (nv <= 2048) p.G = 1024, p.NV = 2;
+        else if (nv <= 4096) p.G = 1024, p.NV = 4;
+    } else if (nv <= 2048) {
+        // 512 threads an SM (1024 for the longest rows): one row of D = 4096
+        // bf16 takes an SM's share of the memory rate about 1000 cycles, a
+        // group's two passes over it about 700
+        if (nv <= 128) p.G = 128, p.NV = 1, p.GR = 4;
+        else if (nv <= 256) p.G = 256, p.NV = 1, p.GR = 2;
+        else if (nv <= 512) p.G = 256, p.NV = 2, p.GR = 2;
+        else if (nv <= 1024) p.G = 512, p.NV = 2, p.GR = 1;
+        else p.G = 1024, p.NV = 2, p.GR = 1;
+        p.stages = static_cast<int>(imin<int64_t>(8, LNB_SMEM / (p.GR * 2 * D * (f32 ? 4 : 2))));
+    }
+    if (p.stages) {
+        p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, 148);
+    } else if (p.G) {
         // blocks for 1024 threads an SM, but no more than there are rows
         const int64_t per = p.G == 32 ? 4 : 1, threads = p.G == 32 ? 128 : p.G;
         p.parts = imin<int64_t>((M + per - 1) / per, 148 * imax<int64_t>(1, 1024 / threads));
@@ -432,19 +575,39 @@ static int launch_layernorm_backward(const LnBackward &a, const LnPlan &p)
     return QFP4_OK;
 }
 
+template <int DT, int G, int NV, int GR, bool KEEP = true>
+static int launch_layernorm_ring(const LnBackward &a, const LnPlan &p)
+{
+    const int smem = GR * p.stages * 2 * static_cast<int>(a.D) * (DT == QFP4_F32 ? 4 : 2);
+    if (ensure_dyn_smem<k_layernorm_backward_ring<DT, G, NV, GR, KEEP>>(LNB_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
+    if (launch_pdl(k_layernorm_backward_ring<DT, G, NV, GR, KEEP>, dim3(static_cast<unsigned>(p.parts)), dim3(GR * G),
+                   smem, a.s, a.dy, a.x, a.M, static_cast<int>(a.D), a.gamma, a.w32, a.mean, a.rstd, a.dx, a.partial,
+                   p.stages) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
+}
+
 template <int DT, int V>
 static int layernorm_backward_by_size(const LnBackward &a, const LnPlan &p)
 {
-    if (p.G == 32) return p.NV == 1 ? launch_layernorm_backward<DT, V, 32, 1>(a, p)
-                                    : launch_layernorm_backward<DT, V, 32, 2>(a, p);
-    if (p.G == 128) return launch_layernorm_backward<DT, V, 128, 1>(a, p);
-    if (p.G == 256) return launch_layernorm_backward<DT, V, 256, 1>(a, p);
-    if (p.G == 512) return launch_layernorm_backward<DT, V, 512, 1>(a, p);
-    if constexpr (V < 8)
-        if (p.NV == 2) return launch_layernorm_backward<DT, V, 1024, 2>(a, p);
-    if constexpr (V == 1)
-        if (p.NV == 4) return launch_layernorm_backward<DT, V, 1024, 4>(a, p);
-    return launch_layernorm_backward<DT, V, 1024, 1>(a, p);
+    if (p.G == 32)
+        return p.NV == 1 ? launch_layernorm_backward<DT, V, 32, 1>(a, p) : launch_layernorm_backward<DT, V, 32, 2>(a, p);
+    if constexpr (V == 1) {
+        if (p.G == 128) return launch_layernorm_backward<DT, 1, 128, 1>(a, p);
+        if (p.G == 512) return launch_layernorm_backward<DT, 1, 512, 1>(a, p);
+        if (p.NV == 1) return launch_layernorm_backward<DT, 1, 1024, 1>(a, p);
+        if (p.NV == 2) return launch_layernorm_backward<DT, 1, 1024, 2>(a, p);
+        return launch_layernorm_backward<DT, 1, 1024, 4>(a, p);
+    } else {
+        if (p.G == 128) return launch_layernorm_ring<DT, 128, 1, 4>(a, p);
+        if (p.G == 256)
+            return p.NV == 1 ? launch_layernorm_ring<DT, 256, 1, 2>(a, p) : launch_layernorm_ring<DT, 256, 2, 2>(a, p);
+        if (p.G == 512) return launch_layernorm_ring<DT, 512, 2, 1>(a, p);
+        return launch_layernorm_ring<DT, 1024, 2, 1, false>(a, p);
+    }
 }
 
 template <int DT>

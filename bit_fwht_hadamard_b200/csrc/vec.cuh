@@ -6,6 +6,79 @@
 
 namespace qfp4 {
 
+// V binary32 values as packed pairs (V = 1: one value), so that sums and
+// products take one instruction for two of them.
+template <int V>
+struct Fv {
+    uint64_t p[V / 2];
+
+    static __device__ __forceinline__ Fv splat(float s)
+    {
+        Fv o;
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) o.p[k] = f2pack(s, s);
+        return o;
+    }
+    static __device__ __forceinline__ Fv of(const float *v)
+    {
+        Fv o;
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) o.p[k] = f2pack(v[2 * k], v[2 * k + 1]);
+        return o;
+    }
+    __device__ __forceinline__ void to(float *v) const
+    {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) f2unpack(p[k], v[2 * k], v[2 * k + 1]);
+    }
+    __device__ __forceinline__ float sum() const
+    {
+        uint64_t a = p[0];
+#pragma unroll
+        for (int k = 1; k < V / 2; ++k) a = f2add(a, p[k]);
+        float x, y;
+        f2unpack(a, x, y);
+        return x + y;
+    }
+};
+template <>
+struct Fv<1> {
+    float p[1];
+    static __device__ __forceinline__ Fv splat(float s) { return Fv{{s}}; }
+    static __device__ __forceinline__ Fv of(const float *v) { return Fv{{v[0]}}; }
+    __device__ __forceinline__ void to(float *v) const { v[0] = p[0]; }
+    __device__ __forceinline__ float sum() const { return p[0]; }
+};
+__device__ __forceinline__ float f2add(float a, float b) { return a + b; }
+__device__ __forceinline__ float f2sub(float a, float b) { return a - b; }
+__device__ __forceinline__ float f2mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float f2fma(float a, float b, float c) { return fmaf(a, b, c); }
+#define QFP4_FV(expr)                                      \
+    Fv<V> o;                                               \
+    _Pragma("unroll") for (int k = 0; k < (V + 1) / 2; ++k) o.p[k] = expr; \
+    return o
+template <int V>
+__device__ __forceinline__ Fv<V> operator+(const Fv<V> &a, const Fv<V> &b)
+{
+    QFP4_FV(f2add(a.p[k], b.p[k]));
+}
+template <int V>
+__device__ __forceinline__ Fv<V> operator-(const Fv<V> &a, const Fv<V> &b)
+{
+    QFP4_FV(f2sub(a.p[k], b.p[k]));
+}
+template <int V>
+__device__ __forceinline__ Fv<V> operator*(const Fv<V> &a, const Fv<V> &b)
+{
+    QFP4_FV(f2mul(a.p[k], b.p[k]));
+}
+template <int V>
+__device__ __forceinline__ Fv<V> fma(const Fv<V> &a, const Fv<V> &b, const Fv<V> &c)
+{
+    QFP4_FV(f2fma(a.p[k], b.p[k], c.p[k]));
+}
+#undef QFP4_FV
+
 // V values of type DT at element i: 16 bytes (V = 8 bf16 or 4 binary32; i a
 // multiple of V), or one value (V = 1).  Raw holds them as loaded.
 template <int DT, int V>
@@ -34,6 +107,18 @@ struct Vec {
             if constexpr (DT == QFP4_F32) v[t] = __uint_as_float(r[t]);
             else v[t] = t & 1 ? bf16hi(r[t >> 1]) : bf16lo(r[t >> 1]);
         }
+    }
+    __device__ __forceinline__ Fv<V> values() const
+    {
+        float v[V];
+        get(v);
+        return Fv<V>::of(v);
+    }
+    __device__ __forceinline__ void set(const Fv<V> &f)
+    {
+        float v[V];
+        f.to(v);
+        set(v);
     }
     // one rounding to DT
     __device__ __forceinline__ void set(const float *v)
@@ -101,6 +186,14 @@ __device__ __forceinline__ void ld_param(const void *p, int f32, int64_t c, floa
     }
 }
 
+template <int V>
+__device__ __forceinline__ Fv<V> ld_param(const void *p, int f32, int64_t c)
+{
+    float v[V];
+    ld_param<V>(p, f32, c, v);
+    return Fv<V>::of(v);
+}
+
 __device__ __forceinline__ float warp_sum(float a)
 {
 #pragma unroll
@@ -124,21 +217,20 @@ __device__ __forceinline__ float group_sum(float a, float *red)
     }
     return a;
 }
+// The same of two values; `bar` is the named barrier of the G threads (their
+// block may hold several groups), which all of them pass once.
 template <int G>
-__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *red)
+__device__ __forceinline__ float2 group_sum2(float a, float b, float2 *red, int bar)
 {
     a = warp_sum(a);
     b = warp_sum(b);
     if constexpr (G > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        a = b = 0.0f;
+        if ((threadIdx.x & 31) == 0) red[(threadIdx.x % G) >> 5] = make_float2(a, b);
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(G) : "memory");
+        uint64_t s = 0ull;                                    // (0, 0)
 #pragma unroll
-        for (int w = 0; w < G / 32; ++w) {
-            const float2 t = red[w];
-            a += t.x;
-            b += t.y;
-        }
+        for (int w = 0; w < G / 32; ++w) s = f2add(s, *reinterpret_cast<const uint64_t *>(red + w));
+        f2unpack(s, a, b);
     }
     return make_float2(a, b);
 }
