@@ -5,26 +5,12 @@
 
 namespace qfp4 {
 
-// Dropout of V values whose first one is element i (i % 4 == 0).
-template <int V>
-__device__ __forceinline__ void drop_values(const DropParams &d, uint64_t step, int64_t i, float *v)
-{
-#pragma unroll
-    for (int g = 0; g < V / 4; ++g) {
-        const uint4 w = drop_words4(d, step, (static_cast<uint64_t>(i) >> 2) + g);
-        v[4 * g] = drop1(d, v[4 * g], w.x);
-        v[4 * g + 1] = drop1(d, v[4 * g + 1], w.y);
-        v[4 * g + 2] = drop1(d, v[4 * g + 2], w.z);
-        v[4 * g + 3] = drop1(d, v[4 * g + 3], w.w);
-    }
-}
-
 // ------------------------------------------------------------------ dropout
 // A thread takes U vectors of 16 bytes, a block's width apart, with all their
 // loads first.
-constexpr int DROP_U = 2;
+constexpr int DROP_U = 4, DROP_BLOCKS = 4;
 template <int DT, bool RES>
-__global__ void __launch_bounds__(256) k_dropout(const void *x, const void *res, int64_t n, DropParams d, void *out)
+__global__ void __launch_bounds__(256, DROP_BLOCKS) k_dropout(const void *x, const void *res, int64_t n, DropParams d, void *out)
 {
     constexpr int V = DT == QFP4_F32 ? 4 : 8;
     pdl_wait();
@@ -44,7 +30,7 @@ __global__ void __launch_bounds__(256) k_dropout(const void *x, const void *res,
         float v[V], s[V];
         if (vec < nvec) {
             a[u].get(v);
-            if (d.on) drop_values<V>(d, step, i, v);
+            if (d.on) drop_values<V, true>(d, step, i, v);
             if (RES) {
                 r[u].get(s);
 #pragma unroll
@@ -54,7 +40,7 @@ __global__ void __launch_bounds__(256) k_dropout(const void *x, const void *res,
             a[u].store(out, i);
         } else if (vec == nvec && i < n) {                  // the last, partial vector
             for (int t = 0; t < V; ++t) v[t] = i + t < n ? ld_as_float(x, DT == QFP4_F32, i + t) : 0.0f;
-            if (d.on) drop_values<V>(d, step, i, v);
+            if (d.on) drop_values<V, true>(d, step, i, v);
             for (int t = 0; t < V && i + t < n; ++t) {
                 if (RES) v[t] += ld_as_float(res, DT == QFP4_F32, i + t);
                 Vec<DT, 1> one;
@@ -138,9 +124,10 @@ static int column_sums(const float *partial, int64_t rows, int64_t N, int TW, in
 // 16-byte accesses; the vectors that straddle a row's ends go element by
 // element.  Reads dY and Z once, writes dZ once: bound by memory.
 constexpr int EB_TILE = 32;                                   // vectors of a block's column tile
+constexpr int EB_U = 1, EB_BLOCKS = 4, EB_WAVE = 4;
 
 // Grid of the kernel: column tiles, row chunks (each a multiple of eight
-// rows) for about six blocks an SM.
+// rows) for EB_WAVE blocks an SM.
 struct EbGrid {
     int tiles, chunks;
     int64_t rows;
@@ -150,18 +137,18 @@ static EbGrid epilogue_backward_grid(int64_t M, int64_t N, int V)
     EbGrid g;
     const int64_t tw = EB_TILE * V;
     g.tiles = static_cast<int>((N % V ? N + V - 1 : N) / tw + ((N % V ? N + V - 1 : N) % tw != 0));
-    const int64_t want = imax<int64_t>(1, imin<int64_t>((6 * 148 + g.tiles - 1) / g.tiles, 512));
+    const int64_t want = imax<int64_t>(1, imin<int64_t>((EB_WAVE * 148 + g.tiles - 1) / g.tiles, 512));
     g.rows = ((M + want - 1) / want + 7) / 8 * 8;
     g.chunks = static_cast<int>((M + g.rows - 1) / g.rows);
     return g;
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const void *z, int64_t M, int64_t N,
+__global__ void __launch_bounds__(256, EB_BLOCKS) k_epilogue_backward(const void *dy, const void *z, int64_t M, int64_t N,
                                                             int64_t rows, int act, DropParams d, void *dz,
                                                             float *partial)
 {
-    constexpr int V = DT == QFP4_F32 ? 4 : 8, U = 2, TW = EB_TILE * V;
+    constexpr int V = DT == QFP4_F32 ? 4 : 8, U = EB_U, TW = EB_TILE * V;
     __shared__ float red[8][TW + V];
     pdl_wait();
     pdl_trigger();
@@ -173,34 +160,45 @@ __global__ void __launch_bounds__(256) k_epilogue_backward(const void *dy, const
     const int64_t m0 = blockIdx.y * rows, m1 = imin(M, m0 + rows);
     const bool use_z = act != QFP4_ACT_NONE;
     Fv<V> sums = Fv<V>::splat(0.0f);
-    for (int64_t m = m0 + w; m < m1; m += 8 * U) {
-        Vec<DT, V> g[U], a[U];
+    // rows m, m + 8, .. of this warp, U at a time; the next ones are loaded
+    // before the present ones are worked on
+    Vec<DT, V> g[U], a[U], gn[U], an[U];
+    auto load = [&](int64_t m, Vec<DT, V> *pg, Vec<DT, V> *pa) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t i = (m + 8 * u) * N + c0;
             if (m + 8 * u < m1 && full) {
-                g[u].load(dy, i);
-                if (use_z) a[u].load(z, i);
+                pg[u].load(dy, i);
+                if (use_z) pa[u].load(z, i);
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) g[u].r[k] = a[u].r[k] = 0u;
+                for (int k = 0; k < 4; ++k) pg[u].r[k] = pa[u].r[k] = 0u;
                 if (m + 8 * u < m1 && some) {
 #pragma unroll
                     for (int t = 0; t < V; ++t)
                         if (c0 + t >= 0 && c0 + t < N) {
-                            g[u].load1(dy, i, t);
-                            if (use_z) a[u].load1(z, i, t);
+                            pg[u].load1(dy, i, t);
+                            if (use_z) pa[u].load1(z, i, t);
                         }
                 }
             }
         }
+    };
+    load(m0 + w, gn, an);
+    for (int64_t m = m0 + w; m < m1; m += 8 * U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            g[u] = gn[u];
+            a[u] = an[u];
+        }
+        load(m + 8 * U, gn, an);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (m + 8 * u >= m1 || !some) continue;
-            const int64_t i = (m + 8 * u) * N + c0;             // a multiple of V; may be -V + 1 .. -1 only with off
+            const int64_t i = (m + 8 * u) * N + c0;             // a multiple of V
             float v[V], x[V];
             g[u].get(v);
-            if (d.on) drop_values<V>(d, step, i, v);
+            if (d.on) drop_values<V, true>(d, step, i, v);
             if (use_z) {
                 a[u].get(x);
                 act_backward<V>(v, x, act);

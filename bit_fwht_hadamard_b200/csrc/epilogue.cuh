@@ -41,10 +41,12 @@ inline DropParams drop_params(double p, uint64_t seed, const uint64_t *step)
 
 __device__ __forceinline__ uint64_t drop_step(const DropParams &d) { return d.on && d.step ? *d.step : 0ull; }
 
-// The four words of elements 4q .. 4q + 3.
-__device__ __forceinline__ uint4 drop_words4(const DropParams &d, uint64_t step, uint64_t q)
+// The four words of elements 4q .. 4q + 3, q = hi 2^32 + lo.  Where a thread
+// takes several quads under one hi, their first product and (from hi and the
+// step alone) one of the second round's are the same, which the compiler sees.
+__device__ __forceinline__ uint4 drop_words4(const DropParams &d, uint64_t step, uint32_t lo, uint32_t hi)
 {
-    uint32_t c0 = static_cast<uint32_t>(q), c1 = static_cast<uint32_t>(q >> 32);
+    uint32_t c0 = lo, c1 = hi;
     uint32_t c2 = static_cast<uint32_t>(step), c3 = static_cast<uint32_t>(step >> 32) | 0x80000000u;
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
@@ -62,44 +64,101 @@ __device__ __forceinline__ float drop1(const DropParams &d, float v, uint32_t wo
     return word >= d.threshold ? __fmul_rn(v, d.scale) : 0.0f;
 }
 
+// Dropout of V values whose first one is element i, in place (i and V are
+// multiples of 4).  ALIGNED: i is a multiple of V too, so that the quads
+// share the counter's high word.
+template <int V, bool ALIGNED>
+__device__ __forceinline__ void drop_values(const DropParams &d, uint64_t step, int64_t i, float *v)
+{
+    const uint64_t q = static_cast<uint64_t>(i) >> 2;
+#pragma unroll
+    for (int g = 0; g < V / 4; ++g) {
+        const uint4 w = drop_words4(d, step, static_cast<uint32_t>(q) + g,
+                                    static_cast<uint32_t>((ALIGNED ? q : q + g) >> 32));
+        v[4 * g] = drop1(d, v[4 * g], w.x);
+        v[4 * g + 1] = drop1(d, v[4 * g + 1], w.y);
+        v[4 * g + 2] = drop1(d, v[4 * g + 2], w.z);
+        v[4 * g + 3] = drop1(d, v[4 * g + 3], w.w);
+    }
+}
+
 // ------------------------------------------------------------------ activations
 // All in binary32 on the unrounded sum z.  A NaN stays a NaN in each of them.
 //
-// The normal distribution function of a pair of values.  Phi(z) - 1/2 is odd
-// and entire, so Phi(z) = 1/2 + z Q(z^2); Q is a polynomial of degree 14 in
-// u = z^2 / 15.125 - 1, fitted by least squares with weights raised towards
-// the largest error, on Chebyshev nodes of |z| <= 5.5 (u in [-1, 1]).  Beyond
-// that Phi is 0 or 1 to 2e-8; the saturation to [0, 1] gives both exactly.
-// Error of Phi below 1.3e-7, of z Phi below 5.6e-7.  Packed multiply-adds, no
-// special-function unit: the library's erff takes about 50 instructions a
-// value (the GEMM's GELU epilogue 311 us against 196 us with this at
-// 8192 x 11008 x 4096).
-__device__ __forceinline__ uint64_t phi2(uint64_t z)
+// GELU on pairs of values, from the normal distribution function of the
+// negative half line: with a = |z| and E = e^(-a^2/2),
+//   Phi(-a) = E m(a),   GELU(z)  = max(z, 0) - a Phi(-a),
+//   Phi(-a) - a phi(a) = E t(a),   GELU'(z) = 1/2 + sign(z) (1/2 - E t(a)).
+// m (Mills' ratio over sqrt(2 pi)) and t = m - a / sqrt(2 pi) are smooth; each
+// is a polynomial of degree 10, fitted on [0, 6] by least squares weighted by
+// E with the weights raised towards the largest error.  E m and E t are then
+// within 1.1e-7 everywhere (a E m within 3.4e-7): E outruns the polynomials
+// beyond 6, and at 16, where a is cut off, it is 2.6e-56, that is 0.  One
+// special-function instruction and five packed multiply-adds a value; erff
+// takes about 50 instructions (the GEMM's GELU epilogue took 311 us with it at
+// 8192 x 11008 x 4096, 215 us with a polynomial).  A NaN stays one.
+__device__ __forceinline__ float abs_upto(float x, float most)
 {
-    float a, b;
-    f2unpack(z, a, b);
-    a = fminf(fmaxf(a, -5.5f), 5.5f);
-    b = fminf(fmaxf(b, -5.5f), 5.5f);
-    const uint64_t c = f2pack(a, b);
-    const uint64_t u = f2fma(f2mul(c, c), f2pack(0.0661157012f, 0.0661157012f), f2pack(-1.0f, -1.0f));
-    uint64_t q = f2pack(0.000549160875f, 0.000549160875f);
-    q = f2fma(q, u, f2pack(-0.00137851201f, -0.00137851201f));
-    q = f2fma(q, u, f2pack(0.000991853536f, 0.000991853536f));
-    q = f2fma(q, u, f2pack(-0.00120224734f, -0.00120224734f));
-    q = f2fma(q, u, f2pack(0.00427189935f, 0.00427189935f));
-    q = f2fma(q, u, f2pack(-0.00770362513f, -0.00770362513f));
-    q = f2fma(q, u, f2pack(0.0104495799f, 0.0104495799f));
-    q = f2fma(q, u, f2pack(-0.014656743f, -0.014656743f));
-    q = f2fma(q, u, f2pack(0.0202930421f, 0.0202930421f));
-    q = f2fma(q, u, f2pack(-0.0261160024f, -0.0261160024f));
-    q = f2fma(q, u, f2pack(0.0320811309f, 0.0320811309f));
-    q = f2fma(q, u, f2pack(-0.0387869067f, -0.0387869067f));
-    q = f2fma(q, u, f2pack(0.0477370173f, 0.0477370173f));
-    q = f2fma(q, u, f2pack(-0.064172484f, -0.064172484f));
-    q = f2fma(q, u, f2pack(0.12855193f, 0.12855193f));
-    float qa, qb;
-    f2unpack(q, qa, qb);
-    return f2pack(__saturatef(fmaf(a, qa, 0.5f)), __saturatef(fmaf(b, qb, 0.5f)));
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %1;\n\tmin.NaN.f32 %0, t, %2;\n\t}" : "=f"(r) : "f"(x), "f"(most));
+    return r;
+}
+__device__ __forceinline__ float max0_nan(float x)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// E of a pair
+__device__ __forceinline__ uint64_t gauss2(uint64_t a)
+{
+    float x, y;
+    f2unpack(f2mul(f2mul(a, f2pack(-0.721347520f, -0.721347520f)), a), x, y);   // -a^2 / 2 log2 e
+    return f2pack(exp2_fast(x), exp2_fast(y));
+}
+__device__ __forceinline__ uint64_t gelu2(float z0, float z1)
+{
+    const uint64_t a = f2pack(abs_upto(z0, 16.0f), abs_upto(z1, 16.0f));
+    const uint64_t na = f2mul(a, f2pack(-1.0f, -1.0f));
+    uint64_t p = f2pack(1.63168431e-06f, 1.63168431e-06f);
+    p = f2fma(p, a, f2pack(-3.52076859e-05f, -3.52076859e-05f));
+    p = f2fma(p, a, f2pack(0.000339737744f, 0.000339737744f));
+    p = f2fma(p, a, f2pack(-0.00197462458f, -0.00197462458f));
+    p = f2fma(p, a, f2pack(0.00793938432f, 0.00793938432f));
+    p = f2fma(p, a, f2pack(-0.0243139211f, -0.0243139211f));
+    p = f2fma(p, a, f2pack(0.0611548796f, 0.0611548796f));
+    p = f2fma(p, a, f2pack(-0.132513791f, -0.132513791f));
+    p = f2fma(p, a, f2pack(0.249916792f, 0.249916792f));
+    p = f2fma(p, a, f2pack(-0.39893651f, -0.39893651f));
+    p = f2fma(p, a, f2pack(0.49999994f, 0.49999994f));
+    return f2fma(f2mul(na, gauss2(a)), p, f2pack(max0_nan(z0), max0_nan(z1)));
+}
+__device__ __forceinline__ uint64_t gelu_slope2(float z0, float z1)
+{
+    const uint64_t a = f2pack(abs_upto(z0, 16.0f), abs_upto(z1, 16.0f));
+    uint64_t p = f2pack(1.63168431e-06f, 1.63168431e-06f);
+    p = f2fma(p, a, f2pack(-3.52076859e-05f, -3.52076859e-05f));
+    p = f2fma(p, a, f2pack(0.000339737744f, 0.000339737744f));
+    p = f2fma(p, a, f2pack(-0.00197462458f, -0.00197462458f));
+    p = f2fma(p, a, f2pack(0.00793938432f, 0.00793938432f));
+    p = f2fma(p, a, f2pack(-0.0243139211f, -0.0243139211f));
+    p = f2fma(p, a, f2pack(0.0611548796f, 0.0611548796f));
+    p = f2fma(p, a, f2pack(-0.132513791f, -0.132513791f));
+    p = f2fma(p, a, f2pack(0.249916792f, 0.249916792f));
+    p = f2fma(p, a, f2pack(-0.797878802f, -0.797878802f));
+    p = f2fma(p, a, f2pack(0.49999994f, 0.49999994f));
+    float x, y;
+    f2unpack(f2fma(f2mul(gauss2(a), f2pack(-1.0f, -1.0f)), p, f2pack(0.5f, 0.5f)), x, y);   // >= -0.13
+    // times the sign of z
+    x = __uint_as_float(__float_as_uint(x) ^ (__float_as_uint(z0) & 0x80000000u));
+    y = __uint_as_float(__float_as_uint(y) ^ (__float_as_uint(z1) & 0x80000000u));
+    return f2add(f2pack(x, y), f2pack(0.5f, 0.5f));
 }
 
 // x within [-most, most]; a NaN stays one.
@@ -110,35 +169,6 @@ __device__ __forceinline__ float clamp_nan(float x, float most)
         : "=f"(r)
         : "f"(x), "f"(most), "f"(-most));
     return r;
-}
-// GELU's slope Phi(z) + z phi(z) of a pair: again 1/2 plus an odd entire
-// function, with a polynomial of degree 17 in u = z^2 / 18 - 1 for |z| <= 6;
-// beyond that it is 0 or 1 to 4e-8.  Error below 2.5e-7.  A NaN stays one.
-__device__ __forceinline__ uint64_t gelu_slope2(uint64_t z)
-{
-    float a, b;
-    f2unpack(z, a, b);
-    const uint64_t c = f2pack(clamp_nan(a, 6.0f), clamp_nan(b, 6.0f));
-    const uint64_t u = f2fma(f2mul(c, c), f2pack(0.055555556f, 0.055555556f), f2pack(-1.0f, -1.0f));
-    uint64_t q = f2pack(-0.00594642246f, -0.00594642246f);
-    q = f2fma(q, u, f2pack(0.0139311319f, 0.0139311319f));
-    q = f2fma(q, u, f2pack(-0.00219016708f, -0.00219016708f));
-    q = f2fma(q, u, f2pack(-0.00573054375f, -0.00573054375f));
-    q = f2fma(q, u, f2pack(-0.026627304f, -0.026627304f));
-    q = f2fma(q, u, f2pack(0.0525551736f, 0.0525551736f));
-    q = f2fma(q, u, f2pack(-0.041894719f, -0.041894719f));
-    q = f2fma(q, u, f2pack(0.0424954034f, 0.0424954034f));
-    q = f2fma(q, u, f2pack(-0.0629948974f, -0.0629948974f));
-    q = f2fma(q, u, f2pack(0.0708191022f, 0.0708191022f));
-    q = f2fma(q, u, f2pack(-0.0650838539f, -0.0650838539f));
-    q = f2fma(q, u, f2pack(0.0579622947f, 0.0579622947f));
-    q = f2fma(q, u, f2pack(-0.0508224741f, -0.0508224741f));
-    q = f2fma(q, u, f2pack(0.04462317f, 0.04462317f));
-    q = f2fma(q, u, f2pack(-0.0423730016f, -0.0423730016f));
-    q = f2fma(q, u, f2pack(0.0460553207f, 0.0460553207f));
-    q = f2fma(q, u, f2pack(-0.0593426675f, -0.0593426675f));
-    q = f2fma(q, u, f2pack(0.117897779f, 0.117897779f));
-    return f2fma(c, q, f2pack(0.5f, 0.5f));
 }
 
 // 1 / (1 + e^-x); 0 for x -> -inf (the fast division gives 0 for a huge
@@ -162,10 +192,7 @@ __device__ __forceinline__ void act_forward(float *v, int act)
         break;
     case QFP4_ACT_GELU:
 #pragma unroll
-        for (int t = 0; t < N; t += 2) {
-            const uint64_t z = f2pack(v[t], v[t + 1]);
-            f2unpack(f2mul(z, phi2(z)), v[t], v[t + 1]);
-        }
+        for (int t = 0; t < N; t += 2) f2unpack(gelu2(v[t], v[t + 1]), v[t], v[t + 1]);
         break;
     case QFP4_ACT_GELU_TANH:
 #pragma unroll
@@ -191,7 +218,7 @@ __device__ __forceinline__ void act_backward(float *d, const float *z, int act)
     case QFP4_ACT_GELU:
 #pragma unroll
         for (int t = 0; t < N; t += 2)
-            f2unpack(f2mul(f2pack(d[t], d[t + 1]), gelu_slope2(f2pack(z[t], z[t + 1]))), d[t], d[t + 1]);
+            f2unpack(f2mul(f2pack(d[t], d[t + 1]), gelu_slope2(z[t], z[t + 1])), d[t], d[t + 1]);
         break;
     case QFP4_ACT_GELU_TANH:
         // beyond |z| = 80 the slope is 0 or 1 to binary32; the clamp keeps z^3 and the products finite
@@ -349,14 +376,7 @@ __device__ __forceinline__ void ep_chunk16(const EpParams &ep, void *out, int64_
     if (ep.preact) row16_store<OUT>(ep.preact, i, v, nc, ep.wide);
     act_forward<16>(v, ep.act);
     if (ep.drop.on) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint4 w = drop_words4(ep.drop, step, (static_cast<uint64_t>(i) >> 2) + g);   // i % 4 == 0
-            v[4 * g] = drop1(ep.drop, v[4 * g], w.x);
-            v[4 * g + 1] = drop1(ep.drop, v[4 * g + 1], w.y);
-            v[4 * g + 2] = drop1(ep.drop, v[4 * g + 2], w.z);
-            v[4 * g + 3] = drop1(ep.drop, v[4 * g + 3], w.w);
-        }
+        drop_values<16, false>(ep.drop, step, i, v);
     }
     if (ep.residual) {
         if (ep.residual_f32) {

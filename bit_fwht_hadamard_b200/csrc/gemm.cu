@@ -159,15 +159,6 @@ __device__ __forceinline__ void reg_fence(uint32_t *r)
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// 1D bulk copy global -> shared, completing on an mbarrier
-__device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // Shared-memory matrix descriptor, K-major, 128-byte swizzle: rows of 128 B,
 // 8-row groups 1024 B apart (SBO), sm_100 descriptor version 1.
 __device__ __forceinline__ uint64_t desc_k_sw128(const void *p)

@@ -23,58 +23,75 @@ __host__ __device__ constexpr int ln_v()
 }
 
 // ------------------------------------------------------------------ forward
-// G threads a row, NV vectors of V elements each: D <= G NV V.
-template <int DT, int V, int G, int NV>
+// G threads take R rows at once, NV vectors of V elements of each: D <= G NV V.
+// The rows stay as they were loaded (unpacking them again for each of the
+// three steps is cheap); R rows share the reads of gamma and beta, which for
+// one row are as many bytes as the row itself and more, and the barriers.
+template <int DT, int V, int G, int NV, int R>
 __global__ void __launch_bounds__(G == 32 ? 128 : G)
     k_layernorm(const void *x, int64_t M, int D, const void *gamma, const void *beta, int w32, float eps, void *y,
                 float *mean_out, float *rstd_out)
 {
-    __shared__ float red[2][G == 32 ? 1 : G / 32];
+    __shared__ float red[2][R][G == 32 ? 1 : G / 32];
     pdl_wait();
     pdl_trigger();
     const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t m = G == 32 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t m = R * (G == 32 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x));
     if (m >= M) return;                                       // a whole group
-    const int64_t r = m * D;
     const int nv = D / V;
-    Vec<DT, V> raw[NV];
+    Vec<DT, V> raw[R][NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (t + k * G < nv) raw[k].load(x, r + static_cast<int64_t>(t + k * G) * V);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv && m + r < M) raw[r][k].load(x, (m + r) * D + static_cast<int64_t>(t + k * G) * V);
     const float inv = 1.0f / static_cast<float>(D);
-    Fv<V> v[NV], s = Fv<V>::splat(0.0f);
+    float mean[R], rstd[R];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (t + k * G < nv) {
-            v[k] = raw[k].values();
-            s = s + v[k];
-        }
-    const float mean = group_sum<G>(s.sum(), red[0]) * inv;
-    const Fv<V> mean2 = Fv<V>::splat(mean);
-    s = Fv<V>::splat(0.0f);
+    for (int r = 0; r < R; ++r) {
+        Fv<V> s = Fv<V>::splat(0.0f);
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (t + k * G < nv) {
-            v[k] = v[k] - mean2;
-            s = fma(v[k], v[k], s);
-        }
-    const float rstd = 1.0f / sqrtf(group_sum<G>(s.sum(), red[1]) * inv + eps);
-    const Fv<V> rstd2 = Fv<V>::splat(rstd);
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) s = s + raw[r][k].values();
+        mean[r] = s.sum();
+    }
+    group_sums<G, R>(mean, red[0]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        mean[r] *= inv;
+        const Fv<V> mean2 = Fv<V>::splat(mean[r]);
+        Fv<V> s = Fv<V>::splat(0.0f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (t + k * G < nv) {
+                const Fv<V> d = raw[r][k].values() - mean2;
+                s = fma(d, d, s);
+            }
+        rstd[r] = s.sum();
+    }
+    group_sums<G, R>(rstd, red[1]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(fmaf(rstd[r], inv, eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         if (t + k * G < nv) {
             const int64_t c = static_cast<int64_t>(t + k * G) * V;
-            Fv<V> o = v[k] * rstd2;
-            if (gamma && beta) o = fma(o, ld_param<V>(gamma, w32, c), ld_param<V>(beta, w32, c));
-            else if (gamma) o = o * ld_param<V>(gamma, w32, c);
-            else if (beta) o = o + ld_param<V>(beta, w32, c);
-            raw[k].set(o);
-            raw[k].store(y, r + c);
+            const Fv<V> g = gamma ? ld_param<V>(gamma, w32, c) : Fv<V>::splat(1.0f);
+            const Fv<V> b = beta ? ld_param<V>(beta, w32, c) : Fv<V>::splat(0.0f);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (m + r < M) {
+                    raw[r][k].set(fma((raw[r][k].values() - Fv<V>::splat(mean[r])) * Fv<V>::splat(rstd[r]), g, b));
+                    raw[r][k].store(y, (m + r) * D + c);
+                }
         }
-    if (t == 0) {
-        if (mean_out) mean_out[m] = mean;
-        if (rstd_out) rstd_out[m] = rstd;
-    }
+    if (t == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (m + r < M) {
+                if (mean_out) mean_out[m + r] = mean[r];
+                if (rstd_out) rstd_out[m + r] = rstd[r];
+            }
 }
 
 // Rows of any length: a block of 1024 a row, three reads of it.
@@ -132,12 +149,13 @@ struct LnForward {
     cudaStream_t s;
 };
 
-template <int DT, int V, int G, int NV>
+template <int DT, int V, int G, int NV, int R>
 static int launch_layernorm(const LnForward &a)
 {
-    const unsigned grid = static_cast<unsigned>(G == 32 ? (a.M + 3) / 4 : a.M);
-    if (launch_pdl(k_layernorm<DT, V, G, NV>, dim3(grid), dim3(G == 32 ? 128 : G), 0, a.s, a.x, a.M,
-                   static_cast<int>(a.D), a.gamma, a.beta, a.w32, a.eps, a.y, a.mean, a.rstd) != cudaSuccess) {
+    const int64_t rows = (a.M + R - 1) / R;
+    if (launch_pdl(k_layernorm<DT, V, G, NV, R>, dim3(static_cast<unsigned>(G == 32 ? (rows + 3) / 4 : rows)),
+                   dim3(G == 32 ? 128 : G), 0, a.s, a.x, a.M, static_cast<int>(a.D), a.gamma, a.beta, a.w32, a.eps, a.y,
+                   a.mean, a.rstd) != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
@@ -145,27 +163,30 @@ static int launch_layernorm(const LnForward &a)
     return QFP4_OK;
 }
 
-// The group of a row: a warp up to 128 vectors; else four vectors a thread,
-// which keeps the most bytes in flight an SM, or, with so few rows that each
-// has an SM to itself, as many threads as there are vectors: the row's own
-// latency is then all there is.
+// The group of a row: a warp up to 64 vectors; else four vectors a thread and
+// LN_ROWS rows at once, which keeps the most bytes in flight an SM.  With so
+// few rows that each has an SM to itself, as many threads as there are
+// vectors: the row's own latency is then all there is.
+constexpr int LN_ROWS = 4;
 template <int DT, int V>
 static int layernorm_by_size(const LnForward &a)
 {
     const int64_t nv = a.D / V;
-    const bool few = a.M <= 2 * 148;
-    if (nv <= 32) return launch_layernorm<DT, V, 32, 1>(a);
-    if (nv <= 64 && !few) return launch_layernorm<DT, V, 32, 2>(a);
-    if (nv <= 128 && !few) return launch_layernorm<DT, V, 32, 4>(a);
-    if (few) {
-        if (nv <= 128) return launch_layernorm<DT, V, 128, 1>(a);
-        if (nv <= 512) return launch_layernorm<DT, V, 512, 1>(a);
-        if (nv <= 1024) return launch_layernorm<DT, V, 1024, 1>(a);
+    if (a.M <= 2 * 148) {
+        if (nv <= 32) return launch_layernorm<DT, V, 32, 1, 1>(a);
+        if (nv <= 128) return launch_layernorm<DT, V, 128, 1, 1>(a);
+        if (nv <= 512) return launch_layernorm<DT, V, 512, 1, 1>(a);
+        if (nv <= 1024) return launch_layernorm<DT, V, 1024, 1, 1>(a);
+        return launch_layernorm<DT, V, 1024, 4, 1>(a);
     }
-    if (nv <= 512) return launch_layernorm<DT, V, 128, 4>(a);
-    if (nv <= 1024) return launch_layernorm<DT, V, 256, 4>(a);
-    if (nv <= 2048) return launch_layernorm<DT, V, 512, 4>(a);
-    return launch_layernorm<DT, V, 1024, 4>(a);
+    if (nv <= 32) return launch_layernorm<DT, V, 32, 1, LN_ROWS>(a);
+    if (nv <= 64) return launch_layernorm<DT, V, 32, 2, LN_ROWS>(a);
+    if (nv <= 128) return launch_layernorm<DT, V, 32, 4, LN_ROWS>(a);
+    if (nv <= 256) return launch_layernorm<DT, V, 64, 4, LN_ROWS>(a);
+    if (nv <= 512) return launch_layernorm<DT, V, 128, 4, LN_ROWS>(a);
+    if (nv <= 1024) return launch_layernorm<DT, V, 256, 4, LN_ROWS>(a);
+    if (nv <= 2048) return launch_layernorm<DT, V, 512, 4, LN_ROWS>(a);
+    return launch_layernorm<DT, V, 1024, 4, 1>(a);
 }
 
 template <int DT>
@@ -319,11 +340,9 @@ __global__ void __launch_bounds__(GR *G, 1)
     pdl_trigger();
     const float inv = 1.0f / static_cast<float>(D);
     const int64_t groups = static_cast<int64_t>(gridDim.x) * GR, m0 = blockIdx.x * static_cast<int64_t>(GR) + gi;
-    // row number it of this group into its stage
-    auto issue = [&](int64_t it) {
-        const int64_t row = m0 + it * groups;
+    // a row into stage s
+    auto issue = [&](int64_t row, int s) {
         if (row >= M) return;
-        const int s = static_cast<int>(it % stages);
         mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
         bulk_g2s(ring + static_cast<size_t>(2 * s) * row_bytes, static_cast<const char *>(dy) + row * row_bytes, row_bytes,
                  &full[s]);
@@ -331,16 +350,25 @@ __global__ void __launch_bounds__(GR *G, 1)
                  &full[s]);
     };
     if (t == 0)
-        for (int i = 0; i < stages - 1; ++i) issue(i);
+        for (int i = 0; i < stages - 1; ++i) issue(m0 + i * groups, i);
     Fv<V> sg[NV], sb[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) sg[k] = sb[k] = Fv<V>::splat(0.0f);
+    float mean_next = 0.0f, rstd_next = 0.0f;
+    if (m0 < M) {
+        mean_next = mean_in[m0];
+        rstd_next = rstd_in[m0];
+    }
     bool ok = true;
-    int64_t it = 0;
-    for (int64_t m = m0; m < M; m += groups, ++it) {
-        const int s = static_cast<int>(it % stages);
-        const float mean = mean_in[m], rstd = rstd_in[m];
-        if (!mbar_wait(&full[s], static_cast<uint32_t>(it / stages) & 1u)) {
+    int s = 0, last = stages - 1;                             // this row's stage, and the row's before it
+    uint32_t phase = 0, par = 0;
+    for (int64_t m = m0; m < M; m += groups) {
+        const float mean = mean_next, rstd = rstd_next;
+        if (m + groups < M) {
+            mean_next = mean_in[m + groups];
+            rstd_next = rstd_in[m + groups];
+        }
+        if (!mbar_wait(&full[s], phase)) {
             ok = false;
             break;
         }
@@ -367,10 +395,16 @@ __global__ void __launch_bounds__(GR *G, 1)
             }
         // this thread's reads of the stages so far come before the next bulk copy
         fence_proxy_async();
-        const float2 c = group_sum2<G>(s1.sum(), s2.sum(), red_sh[gi][it & 1], 1 + gi);
-        // every thread of the group is done with row it - 1, whose stage row
-        // it + stages - 1 takes
-        if (t == 0) issue(it + stages - 1);
+        const float2 c = group_sum2<G>(s1.sum(), s2.sum(), red_sh[gi][par], 1 + gi);
+        // every thread of the group is done with the row before this one,
+        // whose stage takes the row stages - 1 ahead
+        if (t == 0) issue(m + (stages - 1) * groups, last);
+        last = s;
+        par ^= 1u;
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1u;
+        }
         if (!dx) continue;
         const Fv<V> c1 = Fv<V>::splat(c.x * inv), c2 = Fv<V>::splat(c.y * inv);
 #pragma unroll

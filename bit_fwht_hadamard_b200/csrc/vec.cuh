@@ -217,6 +217,25 @@ __device__ __forceinline__ float group_sum(float a, float *red)
     }
     return a;
 }
+// The same of R values each, with one barrier.
+template <int G, int R>
+__device__ __forceinline__ void group_sums(float *a, float (*red)[G == 32 ? 1 : G / 32])
+{
+#pragma unroll
+    for (int r = 0; r < R; ++r) a[r] = warp_sum(a[r]);
+    if constexpr (G > 32) {
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int r = 0; r < R; ++r) red[r][threadIdx.x >> 5] = a[r];
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            a[r] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < G / 32; ++w) a[r] += red[r][w];
+        }
+    }
+}
 // The same of two values; `bar` is the named barrier of the G threads (their
 // block may hold several groups), which all of them pass once.
 template <int G>
