@@ -22,6 +22,7 @@ int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const floa
                      qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream,
                      const EpParams *epi = nullptr);
 size_t gemm_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt);
+size_t gemm_epilogue_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt);
 int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                   const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
                   const EpParams &ep, qfp4_dtype out_dt, void *out, void *workspace, cudaStream_t stream);
@@ -229,7 +230,7 @@ static int epilogue_check(const qfp4_epilogue *e, EpParams *p)
 
 extern "C" size_t qfp4_gemm_epilogue_workspace_bytes(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)
 {
-    return gemm_workspace(M, N, K, fmt);
+    return gemm_epilogue_workspace(M, N, K, fmt);
 }
 
 extern "C" int qfp4_gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale,

@@ -27,6 +27,7 @@
 #include "qfp4_common.cuh"
 #include "quantize1d.cuh"
 #include "epilogue.cuh"
+#include "gemv.cuh"
 
 namespace qfp4 {
 
@@ -1168,8 +1169,23 @@ int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *
         QFP4_LAUNCH_CHECK();
         return QFP4_OK;
     }
+    if (M <= GV_ROWS) {
+        const GemvParams g{A_codes, A_scales, B_codes, B_scales, A_tscale, B_tscale, static_cast<int>(M),
+                           static_cast<int>(N), static_cast<int>(K), out, gemv_split(N, K, fmt == QFP4_MXFP8)};
+        const bool f32 = out_dt == QFP4_F32;
+        if (fmt == QFP4_MXFP8)
+            return f32 ? launch_gemv<QFP4_MXFP8, QFP4_F32>(g, ep, stream) : launch_gemv<QFP4_MXFP8, QFP4_BF16>(g, ep, stream);
+        if (fmt == QFP4_NVFP4)
+            return f32 ? launch_gemv<QFP4_NVFP4, QFP4_F32>(g, ep, stream) : launch_gemv<QFP4_NVFP4, QFP4_BF16>(g, ep, stream);
+        return f32 ? launch_gemv<QFP4_MXFP4, QFP4_F32>(g, ep, stream) : launch_gemv<QFP4_MXFP4, QFP4_BF16>(g, ep, stream);
+    }
     return gemm_blockscaled(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, out_dt, out,
                             workspace, stream, &ep);
+}
+
+size_t gemm_epilogue_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)
+{
+    return M <= GV_ROWS ? 0 : gemm_workspace(M, N, K, fmt);
 }
 
 // ------------------------------------------------------------------ fused rotate + quantize + GEMM
