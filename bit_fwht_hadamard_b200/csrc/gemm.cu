@@ -27,7 +27,6 @@
 #include "qfp4_common.cuh"
 #include "quantize1d.cuh"
 #include "epilogue.cuh"
-#include "gemv.cuh"
 
 namespace qfp4 {
 
@@ -128,6 +127,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// 32 lanes x 16 consecutive fp32 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 // 16 lanes x 128 consecutive fp32 columns (16x256b shape, 16 repetitions):
@@ -1128,6 +1136,12 @@ int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const floa
     return gemm_core(A_codes, sfa, A_tscale, B_codes, sfb, B_tscale, M, N, K, fmt, out_dt, out, stream, epi);
 }
 
+}  // namespace qfp4
+
+#include "gemm_few.cuh"
+
+namespace qfp4 {
+
 // ------------------------------------------------------------------ GEMM with an epilogue
 // K == 0: every sum is zero, the epilogue alone remains.  A thread takes
 // sixteen columns of a row.
@@ -1169,23 +1183,15 @@ int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *
         QFP4_LAUNCH_CHECK();
         return QFP4_OK;
     }
-    if (M <= GV_ROWS) {
-        const GemvParams g{A_codes, A_scales, B_codes, B_scales, A_tscale, B_tscale, static_cast<int>(M),
-                           static_cast<int>(N), static_cast<int>(K), out, gemv_split(N, K, fmt == QFP4_MXFP8)};
-        const bool f32 = out_dt == QFP4_F32;
-        if (fmt == QFP4_MXFP8)
-            return f32 ? launch_gemv<QFP4_MXFP8, QFP4_F32>(g, ep, stream) : launch_gemv<QFP4_MXFP8, QFP4_BF16>(g, ep, stream);
-        if (fmt == QFP4_NVFP4)
-            return f32 ? launch_gemv<QFP4_NVFP4, QFP4_F32>(g, ep, stream) : launch_gemv<QFP4_NVFP4, QFP4_BF16>(g, ep, stream);
-        return f32 ? launch_gemv<QFP4_MXFP4, QFP4_F32>(g, ep, stream) : launch_gemv<QFP4_MXFP4, QFP4_BF16>(g, ep, stream);
-    }
+    if (M <= FW_ROWS)
+        return gemm_few(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, ep, out_dt, out, stream);
     return gemm_blockscaled(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, out_dt, out,
                             workspace, stream, &ep);
 }
 
 size_t gemm_epilogue_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)
 {
-    return M <= GV_ROWS ? 0 : gemm_workspace(M, N, K, fmt);
+    return M <= FW_ROWS ? 0 : gemm_workspace(M, N, K, fmt);
 }
 
 // ------------------------------------------------------------------ fused rotate + quantize + GEMM

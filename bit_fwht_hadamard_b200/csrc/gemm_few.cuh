@@ -1,0 +1,393 @@
+// gemm_few.cuh -- qfp4_gemm_epilogue for up to 128 rows (decoding batches):
+// the weights as the wide operand of the tensor cores.
+//
+// With so few rows of A the call is the reading of B.  So B's rows take the
+// 128 lanes of the accumulator and A's rows (padded to a multiple of 16) its
+// columns: a CTA computes 128 outputs of every row, and the k range is split
+// over a cluster of up to eight CTAs so that most SMs read.  Both operands
+// come by TMA, a ring of k-tiles (128 bytes of a row) deep; the scales go from
+// memory, as the quantize calls write them, through registers into tensor
+// memory (tcgen05.st, as in the pair kernel) with no prepass and no workspace.
+// The CTAs of a cluster add their sums through distributed shared memory, in
+// the order of their k ranges; each then finishes some of the rows.
+#pragma once
+
+#include "epilogue.cuh"
+
+namespace qfp4 {
+
+constexpr int FW_ROWS = 128;               // most rows of A
+constexpr int FW_BN = 128;                 // output columns a CTA
+constexpr int FW_THREADS = 256;            // warps: 0 producer, 1 MMA, 2-3 idle, 4-7 scales; then all epilogue
+constexpr int FW_MAX_STAGES = 10;
+constexpr int FW_SF_BUFS = 5;
+__host__ __device__ constexpr int fw_ahead(int nx) { return nx == 1 ? 8 : 4; }   // k-tiles of scales in registers
+constexpr int FW_MAX_SPLIT = 8;
+constexpr int FW_SMEM_MAX = 208 * 1024;
+
+struct FewParams {
+    const uint8_t *sA, *sB;                // row-major scales: M and N rows of Kg
+    const float *tA, *tB;
+    int M, N, Kg, KT;
+    int rows;                              // M rounded up to 16
+    int split, stages;
+    int aligned;                           // a k-tile's scales of a row are one aligned word group
+    void *out;
+};
+
+__device__ __forceinline__ float ld_dsmem(uint32_t cluster_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// The epilogue of one column of the output, n (this thread's): element i0 + t
+// `stride` elements is row t of the nm rows (at most 16) that exist.
+template <int OUT>
+__device__ __forceinline__ void ep_column16(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nm,
+                                            float alpha, uint64_t step, const float *acc, float bias)
+{
+    float res[16], v[16];
+    if (ep.residual)
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            res[t] = t < nm ? ld_as_float(ep.residual, ep.residual_f32, i0 + t * stride) : 0.0f;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) v[t] = fmaf(acc[t], alpha, bias);
+    auto store = [&](void *p) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            if (t < nm) {
+                if (OUT == QFP4_F32) static_cast<float *>(p)[i0 + t * stride] = v[t];
+                else static_cast<__nv_bfloat16 *>(p)[i0 + t * stride] = __float2bfloat16_rn(v[t]);
+            }
+    };
+    if (ep.preact) store(ep.preact);
+    act_forward<16>(v, ep.act);
+    if (ep.drop.on)
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            if (t < nm) {
+                const uint64_t i = static_cast<uint64_t>(i0 + t * stride), q = i >> 2;
+                const uint4 w = drop_words4(ep.drop, step, static_cast<uint32_t>(q), static_cast<uint32_t>(q >> 32));
+                v[t] = drop1(ep.drop, v[t], i & 2 ? (i & 1 ? w.w : w.z) : (i & 1 ? w.y : w.x));
+            }
+    if (ep.residual)
+#pragma unroll
+        for (int t = 0; t < 16; ++t) v[t] += res[t];
+    store(out);
+}
+
+// NX: 32-row groups of A whose scales are loaded (1 for up to 32 rows, else 4).
+template <int FMT, int OUT, int NX>
+__global__ void __launch_bounds__(FW_THREADS, 1)
+    k_gemm_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, FewParams p, EpParams ep)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) uint64_t full[FW_MAX_STAGES], empty[FW_MAX_STAGES], sf_full[FW_SF_BUFS], sf_empty[FW_SF_BUFS];
+    __shared__ __align__(8) uint64_t acc_full;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ volatile int abort_flag;
+
+    constexpr int CPS = gm_cps(FMT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank()), n0 = static_cast<int>(blockIdx.x / p.split) * FW_BN;
+    const int kt0 = static_cast<int>(static_cast<int64_t>(p.KT) * rank / p.split);
+    const int nkt = static_cast<int>(static_cast<int64_t>(p.KT) * (rank + 1) / p.split) - kt0;   // at least one
+    const int w_bytes = FW_BN * GM_BKB, x_bytes = p.rows * GM_BKB, stage_bytes = w_bytes + x_bytes;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < FW_SF_BUFS; ++b) {
+            mbar_init(&sf_full[b], 4);
+            mbar_init(&sf_empty[b], 1);
+        }
+        mbar_init(&acc_full, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base_sh, GM_TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+    pdl_wait();
+    pdl_trigger();
+
+    auto buf_b = [&](int b) { return tmem + 256 + b * 32; };
+    auto buf_a = [&](int b) { return tmem + 256 + FW_SF_BUFS * 32 + b * 16; };
+
+    if (warp == 0) {
+        // ------------------------------------------------ producer
+        if (lane == 0) {
+            for (int i = 0; i < nkt; ++i) {
+                const int s = i % p.stages;
+                if (!mbar_wait(&empty[s], ((i / p.stages) & 1u) ^ 1u)) { abort_flag = 1; break; }
+                uint8_t *st = smem + static_cast<size_t>(s) * stage_bytes;
+                mbar_arrive_expect_tx(&full[s], stage_bytes);
+                tma_load_2d(st, &tmW, &full[s], (kt0 + i) * GM_BKB, n0);
+                tma_load_2d(st + w_bytes, &tmX, &full[s], (kt0 + i) * GM_BKB, 0);
+            }
+            if (abort_flag) settle_ns(kSettleNs);   // loads already issued may still be landing
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t id = idesc_blockscaled(FMT, FW_BN, p.rows, 0);
+            for (int i = 0; i < nkt; ++i) {
+                const int s = i % p.stages, b = i % FW_SF_BUFS;
+                if (!mbar_wait(&full[s], (i / p.stages) & 1u)) { abort_flag = 1; break; }
+                if (!mbar_wait(&sf_full[b], (i / FW_SF_BUFS) & 1u)) { abort_flag = 1; break; }
+                tc_fence_after();
+                const uint8_t *st = smem + static_cast<size_t>(s) * stage_bytes;
+                const uint64_t wdesc = desc_k_sw128(st), xdesc = desc_k_sw128(st + w_bytes);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_blockscaled<FMT>(tmem, wdesc + 2 * k, xdesc + 2 * k, id, buf_a(b) + 4 * k, buf_b(b) + 8 * k,
+                                          (i | k) != 0);
+                umma_commit(&empty[s]);
+                umma_commit(&sf_empty[b]);
+            }
+            // every MMA this thread issued has finished before the CTA can leave
+            umma_commit(&acc_full);
+            if (!mbar_wait(&acc_full, 0)) abort_flag = 1;
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ scales: this quadrant's 32 rows of B, every row of A
+        constexpr int AHEAD = fw_ahead(NX);
+        const int q = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+        auto load_words = [&](const uint8_t *sc, int R, int row, int kt, uint32_t *w) {
+#pragma unroll
+            for (int c = 0; c < CPS; ++c) w[c] = 0u;
+            if (row >= R || kt >= kt0 + nkt) return;
+            const uint8_t *s = sc + static_cast<int64_t>(row) * p.Kg + 4 * CPS * kt;
+            if (p.aligned) {
+                if constexpr (CPS == 4) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(s);
+                    w[0] = u.x;
+                    w[1] = u.y;
+                    w[2] = u.z;
+                    w[3] = u.w;
+                } else if constexpr (CPS == 2) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(s);
+                    w[0] = u.x;
+                    w[1] = u.y;
+                } else
+                    w[0] = *reinterpret_cast<const uint32_t *>(s);
+            } else
+                for (int i = 0; i < 4 * CPS; ++i)
+                    if (4 * CPS * kt + i < p.Kg) w[i >> 2] |= static_cast<uint32_t>(s[i]) << (8 * (i & 3));
+        };
+        // the scale bytes of this thread's row of B, all of them, into L2: the
+        // loads below reach only AHEAD k-tiles, less than memory's latency
+        if (n0 + 32 * q + lane < p.N) {
+            const uint8_t *s = p.sB + static_cast<int64_t>(n0 + 32 * q + lane) * p.Kg;
+            const int last = imin(4 * CPS * (kt0 + nkt), p.Kg);
+            for (int o = 4 * CPS * kt0; o < last; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(s + o));
+        }
+        uint32_t rw[AHEAD][CPS], rx[AHEAD][NX][CPS];
+        auto load_tile = [&](int kt, int u) {
+            load_words(p.sB, p.N, n0 + 32 * q + lane, kt, rw[u]);
+#pragma unroll
+            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, 32 * m + lane, kt, rx[u][m]);
+        };
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) load_tile(kt0 + u, u);
+        bool ok = true;
+        for (int i0 = 0; i0 < nkt && ok; i0 += AHEAD) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int i = i0 + u, b = i % FW_SF_BUFS;
+                if (i >= nkt || !ok) break;
+                if (!warp_wait(&sf_empty[b], ((i / FW_SF_BUFS) & 1u) ^ 1u)) {
+                    abort_flag = 1;
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // one word per MMA k: a whole raw word (NVFP4), half of one
+                // (MXFP4, its two scales in bytes 0-1) or a byte (MXFP8)
+                auto mma_word = [&](const uint32_t *raw, int k) -> uint32_t {
+                    if constexpr (FMT == QFP4_NVFP4) return raw[k];
+                    else if constexpr (FMT == QFP4_MXFP4) return (raw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+                    else return (raw[0] >> (8 * k)) & 0xFFu;
+                };
+                uint32_t av[16], bv[32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t wa = mma_word(rw[u], k);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        av[4 * k + c] = wa;
+                        bv[8 * k + c] = c < NX ? mma_word(rx[u][c < NX ? c : 0], k) : 0u;
+                        bv[8 * k + 4 + c] = 0u;
+                    }
+                }
+                tmem_st_x16(buf_a(b) + lane_base, av);
+                tmem_st_x32(buf_b(b) + lane_base, bv);
+                load_tile(kt0 + i + AHEAD, u);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sf_full[b]);
+            }
+        }
+    }
+    // ---------------------------------------------------- this CTA's sums: all
+    // eight warps, a quadrant of outputs and every other 16 rows each
+    __syncwarp();
+    const int q = warp & 3, half = warp >> 2, n = n0 + 32 * q + lane;
+    const uint32_t acc_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const bool ok = warp_wait(&acc_full, 0) && !abort_flag;
+    tc_fence_after();
+    float alpha = 1.0f;
+    if (FMT == QFP4_NVFP4) alpha = __fmul_rn(*p.tA, *p.tB);
+    const uint64_t step = drop_step(ep.drop);
+    const float bias = ep.bias && n < p.N ? ld_as_float(ep.bias, ep.bias_f32, n) : 0.0f;
+    float *sums = reinterpret_cast<float *>(smem);            // [row][128], once every stage has been read (acc_full)
+    for (int m0 = 16 * half; m0 < p.rows; m0 += 32) {
+        uint32_t r[16];
+        tmem_ld16(acc_lane + m0, r);
+        tmem_ld_wait();
+        reg_fence<16>(r);
+        float v[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) v[t] = __uint_as_float(r[t]);
+        if (p.split > 1) {
+#pragma unroll
+            for (int t = 0; t < 16; ++t) sums[(m0 + t) * FW_BN + 32 * q + lane] = v[t];
+        } else if (ok && n < p.N)
+            ep_column16<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, p.N, p.M - m0, alpha, step, v, bias);
+        __syncwarp();
+    }
+    if (p.split > 1) {
+        cluster_sync();                                       // every CTA's sums are in its shared memory
+        // rows rank, rank + split, ..: 16 of them at a time, the two halves in turn
+        const uint32_t base = smem_u32(smem) + 4 * (32 * q + lane);
+        if (ok && n < p.N)
+            for (int m0 = rank + 16 * half * p.split; m0 < p.M; m0 += 32 * p.split) {
+                float v[16];
+                const int nm = imin(16, (p.M - m0 + p.split - 1) / p.split);
+                const uint32_t from = base + 4 * FW_BN * m0;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    float x[FW_MAX_SPLIT];
+#pragma unroll
+                    for (int r = 0; r < FW_MAX_SPLIT; ++r) {
+                        x[r] = 0.0f;
+                        if (t < nm && r < p.split) x[r] = ld_dsmem(mapa_shared(from + 4 * FW_BN * p.split * t, r));
+                    }
+                    v[t] = x[0];
+#pragma unroll
+                    for (int r = 1; r < FW_MAX_SPLIT; ++r) v[t] += x[r];
+                }
+                ep_column16<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
+                                 alpha, step, v, bias);
+            }
+        __syncwarp();
+        cluster_sync();                                       // nobody reads this CTA's shared memory any more
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, GM_TMEM_COLS);
+}
+
+template <int FMT, int OUT, int NX>
+static int launch_few_nx(const CUtensorMap &tw, const CUtensorMap &tx, const FewParams &p, const EpParams &ep, int smem,
+                      cudaStream_t s)
+{
+    if (ensure_dyn_smem<k_gemm_few<FMT, OUT, NX>>(FW_SMEM_MAX + 1024) != QFP4_OK) return QFP4_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((p.N + FW_BN - 1) / FW_BN * p.split), 1, 1);
+    cfg.blockDim = dim3(FW_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, k_gemm_few<FMT, OUT, NX>, tw, tx, p, ep) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return QFP4_ERR_CUDA;
+    }
+    QFP4_LAUNCH_CHECK();
+    return QFP4_OK;
+}
+
+template <int FMT, int OUT>
+static int launch_few(const CUtensorMap &tw, const CUtensorMap &tx, const FewParams &p, const EpParams &ep, int smem,
+                      cudaStream_t s)
+{
+    return p.rows <= 32 ? launch_few_nx<FMT, OUT, 1>(tw, tx, p, ep, smem, s)
+                        : launch_few_nx<FMT, OUT, 4>(tw, tx, p, ep, smem, s);
+}
+
+static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
+                    const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
+                    const EpParams &ep, qfp4_dtype out_dt, void *out, cudaStream_t stream)
+{
+    FewParams p;
+    p.sA = A_scales;
+    p.sB = B_scales;
+    p.tA = A_tscale;
+    p.tB = B_tscale;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(N);
+    p.Kg = static_cast<int>(K / (fmt == QFP4_NVFP4 ? 16 : 32));
+    p.KT = static_cast<int>((K + gm_bk(fmt) - 1) / gm_bk(fmt));
+    p.rows = static_cast<int>((M + 15) / 16 * 16);
+    p.aligned = K % gm_bk(fmt) == 0;
+    p.out = out;
+    // as many CTAs as there are SMs, by splitting K (a CTA keeps two k-tiles at least)
+    const int64_t tiles = (N + FW_BN - 1) / FW_BN;
+    p.split = static_cast<int>(imax<int64_t>(1, imin<int64_t>(imin<int64_t>(FW_MAX_SPLIT, 148 / tiles), p.KT / 2)));
+    // all of a CTA's k-tiles under way at once, where shared memory allows
+    const int stage = (FW_BN + p.rows) * GM_BKB;
+    const int per = (p.KT + p.split - 1) / p.split;
+    p.stages = imax(2, imin(imin(FW_MAX_STAGES, per), FW_SMEM_MAX / stage));
+    const int smem = imax(p.stages * stage, p.split > 1 ? p.rows * FW_BN * 4 : 0) + 1024;
+    CUtensorMap tw, tx;
+    const uint64_t row_bytes = static_cast<uint64_t>(fmt == QFP4_MXFP8 ? K : K / 2);
+    {
+        const uint64_t dims[2] = {row_bytes, static_cast<uint64_t>(N)}, strides[1] = {row_bytes};
+        const uint32_t box[2] = {GM_BKB, FW_BN};
+        const int st = encode_tensor_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(B_codes), dims,
+                                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != QFP4_OK) return st;
+    }
+    {
+        const uint64_t dims[2] = {row_bytes, static_cast<uint64_t>(M)}, strides[1] = {row_bytes};
+        const uint32_t box[2] = {GM_BKB, static_cast<uint32_t>(p.rows)};
+        const int st = encode_tensor_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(A_codes), dims,
+                                         strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != QFP4_OK) return st;
+    }
+    const bool f32 = out_dt == QFP4_F32;
+    if (fmt == QFP4_MXFP8)
+        return f32 ? launch_few<QFP4_MXFP8, QFP4_F32>(tw, tx, p, ep, smem, stream)
+                   : launch_few<QFP4_MXFP8, QFP4_BF16>(tw, tx, p, ep, smem, stream);
+    if (fmt == QFP4_NVFP4)
+        return f32 ? launch_few<QFP4_NVFP4, QFP4_F32>(tw, tx, p, ep, smem, stream)
+                   : launch_few<QFP4_NVFP4, QFP4_BF16>(tw, tx, p, ep, smem, stream);
+    return f32 ? launch_few<QFP4_MXFP4, QFP4_F32>(tw, tx, p, ep, smem, stream)
+               : launch_few<QFP4_MXFP4, QFP4_BF16>(tw, tx, p, ep, smem, stream);
+}
+
+}  // namespace qfp4
