@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[G2_STAGES], empty[G2_STAGES], sfs_full[G2_SF_SLOTS], sfs_empty[G2_SF_SLOTS];
-    __shared__ __align__(8) uint64_t sf_full[G2_SF_BUFS_MAX], sf_empty[G2_SF_BUFS_MAX], acc_full, acc_empty, drain;
+    __shared__ __align__(8) uint64_t acc_full, acc_empty, drain;
     __shared__ float4 bias_sh[EP ? 2 : 1][EP ? 64 : 1];   // by tile parity
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
@@ -661,16 +661,12 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < G2_STAGES; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + 2 * G2_SF_WARPS);
             mbar_init(&empty[s], 1);
         }
         for (int s = 0; s < G2_SF_SLOTS; ++s) {
             mbar_init(&sfs_full[s], 1);
             mbar_init(&sfs_empty[s], G2_SF_WARPS);
-        }
-        for (int b = 0; b < NBUF; ++b) {
-            mbar_init(&sf_full[b], 2 * G2_SF_WARPS);
-            mbar_init(&sf_empty[b], 1);
         }
         mbar_init(&acc_full, 1);
         mbar_init(&acc_empty, 2 * GM_EPI_WARPS);
@@ -732,25 +728,37 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
         } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader CTA only)
         if (leader && lane == 0) {
-            int it = 0, ti = 0;
+            // One thread issues everything, and each of its instructions that
+            // touches a barrier or the tensor pipe takes it 60 to 100 cycles;
+            // a k-tile's MMAs take the pipe 514.  So a k-tile has one barrier
+            // (operands and scales) and one commit, and the next k-tile's
+            // barrier is tested before this one's MMAs are issued.
+            int s = 0, b = 0, ti = 0;
+            uint32_t ph = 0;
+            bool ready = false;
             for (int t = cluster; t < ntiles && !abort_flag; t += nclusters, ++ti) {
                 if (!mbar_wait(&acc_empty, (ti & 1) ^ 1u)) { abort_flag = 1; break; }
                 tc_fence_after();
-                for (int kt = 0; kt < p.KT; ++kt, ++it) {
-                    const int s = it % G2_STAGES, b = it % NBUF;
-                    if (!mbar_wait(&full[s], (it / G2_STAGES) & 1u)) { abort_flag = 1; break; }
-                    if (!mbar_wait(&sf_full[b], (it / NBUF) & 1u)) { abort_flag = 1; break; }
+                for (int kt = 0; kt < p.KT; ++kt) {
+                    if (!ready && !mbar_wait(&full[s], ph)) { abort_flag = 1; break; }
                     tc_fence_after();
                     const uint64_t adesc = desc_k_sw128(stage_a(s));
                     const uint64_t bdesc = desc_k_sw128(stage_b(s));
+                    const uint32_t sa = buf_a(b), sb = buf_b(b);
+                    uint64_t *done = &empty[s];
+                    if (++s == G2_STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (++b == NBUF) b = 0;
+                    ready = mbar_test(&full[s], ph);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {       // four MMAs of 64 (FP4) or 32 (FP8) elements
                         umma_blockscaled_cg2<FMT>(tmem, adesc + 2 * k, bdesc + 2 * k,
-                                                  idesc_blockscaled(FMT, G2_BM, G2_BN, 0), buf_a(b) + 4 * k,
-                                                  buf_b(b) + 8 * k, (kt | k) != 0);
+                                                  idesc_blockscaled(FMT, G2_BM, G2_BN, 0), sa + 4 * k, sb + 8 * k,
+                                                  (kt | k) != 0);
                     }
-                    umma_commit_cg2_both(&empty[s]);
-                    umma_commit_cg2_both(&sf_empty[b]);
+                    umma_commit_cg2_both(done);
                 }
                 umma_commit_cg2_both(&acc_full);
             }
@@ -790,44 +798,64 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
         // ------------------------------------------------ scale warps (both CTAs: own TMEM quadrant)
         const int q = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-        int it = 0;
-        for (int t = cluster; t < ntiles && !abort_flag; t += nclusters) {
-            for (int kt = 0; kt < p.KT; ++kt, ++it) {
-                const int s = it % G2_SF_SLOTS, b = it % NBUF;
-                if (!warp_wait(&sfs_full[s], (it / G2_SF_SLOTS) & 1u)) { abort_flag = 1; break; }
-                if (!warp_wait(&sf_empty[b], ((it / NBUF) & 1u) ^ 1u)) { abort_flag = 1; break; }
-                tc_fence_after();
-                // raw scale words of this k-tile: word w = the four scales of
-                // k-groups 4w .. 4w + 3 (CPS words per row)
-                uint32_t ra[CPS], rb[2][CPS][4];
-                const uint8_t *sa = slot_sfa(s) + lane * 16 + q * 4;
+        // raw scale words of a k-tile: word w = the four scales of k-groups
+        // 4w .. 4w + 3 (CPS words per row)
+        uint32_t ra[CPS], rb[2][CPS][4];
+        int slot = 0;
+        uint32_t slot_ph = 0;
+        auto load_slot = [&]() -> bool {
+            if (!warp_wait(&sfs_full[slot], slot_ph)) return false;
+            const uint8_t *sa = slot_sfa(slot) + lane * 16 + q * 4;
 #pragma unroll
-                for (int w = 0; w < CPS; ++w) ra[w] = *reinterpret_cast<const uint32_t *>(sa + 512 * w);
+            for (int w = 0; w < CPS; ++w) ra[w] = *reinterpret_cast<const uint32_t *>(sa + 512 * w);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int w = 0; w < CPS; ++w) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(slot_sfb(s) + 512 * (h * CPS + w) + lane * 16);
-                        rb[h][w][0] = u.x;
-                        rb[h][w][1] = u.y;
-                        rb[h][w][2] = u.z;
-                        rb[h][w][3] = u.w;
-                    }
-                // The slot is refilled by the scale producer's next TMA load (an
-                // async-proxy write); the reads above are generic-proxy accesses
-                // that may still be outstanding when the release below issues.
-                // The proxy fence in every lane orders them before the refill.
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sfs_empty[s]);
-                // one TMEM word per MMA k: NVFP4 (K = 64) uses a whole raw word,
-                // MXFP4 (K = 64) the half of one (its two block-32 scales, in
-                // bytes 0-1), MXFP8 (K = 32) one byte (its one block-32 scale)
-                auto mma_word = [&](const uint32_t *raw, int k) -> uint32_t {
-                    if constexpr (FMT == QFP4_NVFP4) return raw[k];
-                    else if constexpr (FMT == QFP4_MXFP4) return (raw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
-                    else return (raw[0] >> (8 * k)) & 0xFFu;
-                };
+                for (int w = 0; w < CPS; ++w) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(slot_sfb(slot) + 512 * (h * CPS + w) + lane * 16);
+                    rb[h][w][0] = u.x;
+                    rb[h][w][1] = u.y;
+                    rb[h][w][2] = u.z;
+                    rb[h][w][3] = u.w;
+                }
+            // The slot is refilled by the scale producer's next TMA load (an
+            // async-proxy write); the reads above are generic-proxy accesses
+            // that may still be outstanding when the release below issues.
+            // The proxy fence in every lane orders them before the refill.
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfs_empty[slot]);
+            if (++slot == G2_SF_SLOTS) {
+                slot = 0;
+                slot_ph ^= 1u;
+            }
+            return true;
+        };
+        // A buffer is free again once the k-tile NBUF before has its MMAs done,
+        // which is that k-tile's stage released: old_s / old_ph follow it.
+        int s = 0, b = 0, old_s = 0, it = 0;
+        uint32_t old_ph = 0;
+        int left = 0;                                        // k-tiles of this cluster's tiles
+        for (int t = cluster; t < ntiles; t += nclusters) left += p.KT;
+        bool ok = left == 0 || load_slot();
+        for (; left > 0 && ok; --left, ++it) {
+            if (it >= NBUF) {
+                if (!warp_wait(&empty[old_s], old_ph)) break;
+                if (++old_s == G2_STAGES) {
+                    old_s = 0;
+                    old_ph ^= 1u;
+                }
+            }
+            tc_fence_after();
+            // one TMEM word per MMA k: NVFP4 (K = 64) uses a whole raw word,
+            // MXFP4 (K = 64) the half of one (its two block-32 scales, in
+            // bytes 0-1), MXFP8 (K = 32) one byte (its one block-32 scale)
+            auto mma_word = [&](const uint32_t *raw, int k) -> uint32_t {
+                if constexpr (FMT == QFP4_NVFP4) return raw[k];
+                else if constexpr (FMT == QFP4_MXFP4) return (raw[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+                else return (raw[0] >> (8 * k)) & 0xFFu;
+            };
+            {
                 uint32_t av[16], bv[32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -846,16 +874,17 @@ __global__ void __launch_bounds__(G2_THREADS, 1)
                 }
                 tmem_st_x16(buf_a(b) + lane_base, av);
                 tmem_st_x32(buf_b(b) + lane_base, bv);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sf_full[b]), 0));
             }
+            // the next k-tile's words come while these stores complete
+            if (left > 1) ok = load_slot();
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[s]), 0));
+            if (++s == G2_STAGES) s = 0;
+            if (++b == NBUF) b = 0;
         }
-        // the leader's last releases of the scale buffers are multicast into
-        // this CTA too: let them land before the CTA can leave
-        for (int i = 0; i < NBUF && !abort_flag; ++i, ++it)
-            if (!warp_wait(&sf_empty[it % NBUF], ((it / NBUF) & 1u) ^ 1u)) abort_flag = 1;
+        if (left > 0) abort_flag = 1;
         g2_exit(tmem, false);
         return;
     }
