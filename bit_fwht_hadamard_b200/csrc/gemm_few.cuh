@@ -18,10 +18,12 @@ namespace qfp4 {
 
 constexpr int FW_ROWS = 128;               // most rows of A
 constexpr int FW_BN = 128;                 // output columns a CTA
-constexpr int FW_THREADS = 256;            // warps: 0 producer, 1 MMA, 2-3 idle, 4-7 scales; then all epilogue
+// warps: 0 and 2 producers of B and A, 1 MMA, 3 idle, 4-7 and 8-11 scales of
+// the even and the odd k-tiles; the first eight then finish the sums
+constexpr int FW_THREADS = 384;
 constexpr int FW_MAX_STAGES = 10;
 constexpr int FW_SF_BUFS = 5;
-__host__ __device__ constexpr int fw_ahead(int nx) { return nx == 1 ? 8 : 4; }   // k-tiles of scales in registers
+__host__ __device__ constexpr int fw_ahead(int nx) { return nx == 1 ? 4 : 2; }   // k-tiles of scales in registers a warp
 constexpr int FW_MAX_SPLIT = 8;
 constexpr int FW_SMEM_MAX = 208 * 1024;
 
@@ -43,39 +45,42 @@ __device__ __forceinline__ float ld_dsmem(uint32_t cluster_addr)
 }
 
 // The epilogue of one column of the output, n (this thread's): element i0 + t
-// `stride` elements is row t of the nm rows (at most 16) that exist.
+// `stride` elements is row t of the nm rows (at most FW_EP) that exist.  Few
+// rows at a time, so that the code stays short: with a row or two to finish,
+// fetching it is what the epilogue costs (sixteen at a time took 3 us more).
+constexpr int FW_EP = 4;
 template <int OUT>
-__device__ __forceinline__ void ep_column16(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nm,
-                                            float alpha, uint64_t step, const float *acc, float bias)
+__device__ __forceinline__ void ep_column(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nm,
+                                          float alpha, uint64_t step, const float *acc, float bias)
 {
-    float res[16], v[16];
+    float res[FW_EP], v[FW_EP];
     if (ep.residual)
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
+        for (int t = 0; t < FW_EP; ++t)
             res[t] = t < nm ? ld_as_float(ep.residual, ep.residual_f32, i0 + t * stride) : 0.0f;
 #pragma unroll
-    for (int t = 0; t < 16; ++t) v[t] = fmaf(acc[t], alpha, bias);
+    for (int t = 0; t < FW_EP; ++t) v[t] = fmaf(acc[t], alpha, bias);
     auto store = [&](void *p) {
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
+        for (int t = 0; t < FW_EP; ++t)
             if (t < nm) {
                 if (OUT == QFP4_F32) static_cast<float *>(p)[i0 + t * stride] = v[t];
                 else static_cast<__nv_bfloat16 *>(p)[i0 + t * stride] = __float2bfloat16_rn(v[t]);
             }
     };
     if (ep.preact) store(ep.preact);
-    act_forward<16>(v, ep.act);
-    if (ep.drop.on)
+    act_forward<FW_EP>(v, ep.act);
+    if (ep.drop.on) {
 #pragma unroll
-        for (int t = 0; t < 16; ++t)
-            if (t < nm) {
-                const uint64_t i = static_cast<uint64_t>(i0 + t * stride), q = i >> 2;
-                const uint4 w = drop_words4(ep.drop, step, static_cast<uint32_t>(q), static_cast<uint32_t>(q >> 32));
-                v[t] = drop1(ep.drop, v[t], i & 2 ? (i & 1 ? w.w : w.z) : (i & 1 ? w.y : w.x));
-            }
+        for (int t = 0; t < FW_EP; ++t) {
+            const uint64_t i = static_cast<uint64_t>(i0 + t * stride), q = i >> 2;
+            const uint4 w = drop_words4(ep.drop, step, static_cast<uint32_t>(q), static_cast<uint32_t>(q >> 32));
+            v[t] = drop1(ep.drop, v[t], i & 2 ? (i & 1 ? w.w : w.z) : (i & 1 ? w.y : w.x));
+        }
+    }
     if (ep.residual)
 #pragma unroll
-        for (int t = 0; t < 16; ++t) v[t] += res[t];
+        for (int t = 0; t < FW_EP; ++t) v[t] += res[t];
     store(out);
 }
 
@@ -86,8 +91,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[FW_MAX_STAGES], empty[FW_MAX_STAGES], sf_full[FW_SF_BUFS], sf_empty[FW_SF_BUFS];
-    __shared__ __align__(8) uint64_t acc_full;
+    __shared__ __align__(8) uint64_t full[FW_MAX_STAGES], empty[FW_MAX_STAGES], acc_full;
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
 
@@ -100,12 +104,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2 + 4);                       // two producers, four scale warps
             mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < FW_SF_BUFS; ++b) {
-            mbar_init(&sf_full[b], 4);
-            mbar_init(&sf_empty[b], 1);
         }
         mbar_init(&acc_full, 1);
         abort_flag = 0;
@@ -127,16 +127,24 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     auto buf_b = [&](int b) { return tmem + 256 + b * 32; };
     auto buf_a = [&](int b) { return tmem + 256 + FW_SF_BUFS * 32 + b * 16; };
 
-    if (warp == 0) {
-        // ------------------------------------------------ producer
+    // A k-tile has one barrier (operands and scales) and one commit: each
+    // instruction on a barrier or the tensor pipe takes the thread that issues
+    // it 60 to 100 cycles, and with so few columns that is all a k-tile costs.
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------ producers
         if (lane == 0) {
+            const CUtensorMap *map = warp == 0 ? &tmW : &tmX;
+            const int bytes = warp == 0 ? w_bytes : x_bytes, row = warp == 0 ? n0 : 0, off = warp == 0 ? 0 : w_bytes;
+            int s = 0;
+            uint32_t ph = 1;
             for (int i = 0; i < nkt; ++i) {
-                const int s = i % p.stages;
-                if (!mbar_wait(&empty[s], ((i / p.stages) & 1u) ^ 1u)) { abort_flag = 1; break; }
-                uint8_t *st = smem + static_cast<size_t>(s) * stage_bytes;
-                mbar_arrive_expect_tx(&full[s], stage_bytes);
-                tma_load_2d(st, &tmW, &full[s], (kt0 + i) * GM_BKB, n0);
-                tma_load_2d(st + w_bytes, &tmX, &full[s], (kt0 + i) * GM_BKB, 0);
+                if (i >= p.stages && !mbar_wait(&empty[s], ph)) { abort_flag = 1; break; }
+                mbar_arrive_expect_tx(&full[s], bytes);
+                tma_load_2d(smem + static_cast<size_t>(s) * stage_bytes + off, map, &full[s], (kt0 + i) * GM_BKB, row);
+                if (++s == p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
             if (abort_flag) settle_ns(kSettleNs);   // loads already issued may still be landing
         }
@@ -144,19 +152,26 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         // ------------------------------------------------ MMA issuer
         if (lane == 0) {
             const uint32_t id = idesc_blockscaled(FMT, FW_BN, p.rows, 0);
+            int s = 0, b = 0;
+            uint32_t ph = 0;
+            bool ready = false;
             for (int i = 0; i < nkt; ++i) {
-                const int s = i % p.stages, b = i % FW_SF_BUFS;
-                if (!mbar_wait(&full[s], (i / p.stages) & 1u)) { abort_flag = 1; break; }
-                if (!mbar_wait(&sf_full[b], (i / FW_SF_BUFS) & 1u)) { abort_flag = 1; break; }
+                if (!ready && !mbar_wait(&full[s], ph)) { abort_flag = 1; break; }
                 tc_fence_after();
                 const uint8_t *st = smem + static_cast<size_t>(s) * stage_bytes;
                 const uint64_t wdesc = desc_k_sw128(st), xdesc = desc_k_sw128(st + w_bytes);
+                const uint32_t sa = buf_a(b), sb = buf_b(b);
+                uint64_t *done = &empty[s];
+                if (++s == p.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++b == FW_SF_BUFS) b = 0;
+                ready = mbar_test(&full[s], ph);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    umma_blockscaled<FMT>(tmem, wdesc + 2 * k, xdesc + 2 * k, id, buf_a(b) + 4 * k, buf_b(b) + 8 * k,
-                                          (i | k) != 0);
-                umma_commit(&empty[s]);
-                umma_commit(&sf_empty[b]);
+                    umma_blockscaled<FMT>(tmem, wdesc + 2 * k, xdesc + 2 * k, id, sa + 4 * k, sb + 8 * k, (i | k) != 0);
+                umma_commit(done);
             }
             // every MMA this thread issued has finished before the CTA can leave
             umma_commit(&acc_full);
@@ -165,7 +180,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     } else if (warp >= 4) {
         // ------------------------------------------------ scales: this quadrant's 32 rows of B, every row of A
         constexpr int AHEAD = fw_ahead(NX);
-        const int q = warp & 3;
+        const int q = warp & 3, odd = warp >= 8 ? 1 : 0;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
         auto load_words = [&](const uint8_t *sc, int R, int row, int kt, uint32_t *w) {
 #pragma unroll
@@ -190,27 +205,32 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
                     if (4 * CPS * kt + i < p.Kg) w[i >> 2] |= static_cast<uint32_t>(s[i]) << (8 * (i & 3));
         };
         // the scale bytes of this thread's row of B, all of them, into L2: the
-        // loads below reach only AHEAD k-tiles, less than memory's latency
-        if (n0 + 32 * q + lane < p.N) {
+        // loads below reach only a few k-tiles, less than memory's latency
+        if (n0 + 32 * q + lane < p.N && !odd) {
             const uint8_t *s = p.sB + static_cast<int64_t>(n0 + 32 * q + lane) * p.Kg;
             const int last = imin(4 * CPS * (kt0 + nkt), p.Kg);
             for (int o = 4 * CPS * kt0; o < last; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(s + o));
         }
         uint32_t rw[AHEAD][CPS], rx[AHEAD][NX][CPS];
-        auto load_tile = [&](int kt, int u) {
-            load_words(p.sB, p.N, n0 + 32 * q + lane, kt, rw[u]);
+        auto load_tile = [&](int i, int u) {                  // k-tile i of this CTA
+            load_words(p.sB, p.N, n0 + 32 * q + lane, kt0 + i, rw[u]);
 #pragma unroll
-            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, 32 * m + lane, kt, rx[u][m]);
+            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, 32 * m + lane, kt0 + i, rx[u][m]);
         };
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) load_tile(kt0 + u, u);
+        for (int u = 0; u < AHEAD; ++u) load_tile(odd + 2 * u, u);
+        // k-tile i has scale buffer i mod FW_SF_BUFS, which k-tile
+        // i - FW_SF_BUFS has left when its stage is released, and arrives on
+        // the barrier of stage i mod stages
+        int b = odd, s = odd % p.stages, old_s = (odd + p.stages * FW_SF_BUFS - FW_SF_BUFS) % p.stages;
+        int old_round = -((FW_SF_BUFS - odd + p.stages - 1) / p.stages);   // floor((odd - FW_SF_BUFS) / stages)
         bool ok = true;
-        for (int i0 = 0; i0 < nkt && ok; i0 += AHEAD) {
+        for (int i0 = odd; i0 < nkt && ok; i0 += 2 * AHEAD) {
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
-                const int i = i0 + u, b = i % FW_SF_BUFS;
+                const int i = i0 + 2 * u;
                 if (i >= nkt || !ok) break;
-                if (!warp_wait(&sf_empty[b], ((i / FW_SF_BUFS) & 1u) ^ 1u)) {
+                if (i >= FW_SF_BUFS && !warp_wait(&empty[old_s], static_cast<uint32_t>(old_round) & 1u)) {
                     abort_flag = 1;
                     ok = false;
                     break;
@@ -236,18 +256,27 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
                 }
                 tmem_st_x16(buf_a(b) + lane_base, av);
                 tmem_st_x32(buf_b(b) + lane_base, bv);
-                load_tile(kt0 + i + AHEAD, u);
+                load_tile(i + 2 * AHEAD, u);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sf_full[b]);
+                if (lane == 0) mbar_arrive(&full[s]);
+                // two k-tiles on
+                b = b + 2 >= FW_SF_BUFS ? b + 2 - FW_SF_BUFS : b + 2;
+                s += 2;
+                if (s >= p.stages) s -= p.stages;
+                old_s += 2;
+                if (old_s >= p.stages) {
+                    old_s -= p.stages;
+                    ++old_round;
+                }
             }
         }
     }
     // ---------------------------------------------------- this CTA's sums: all
     // eight warps, a quadrant of outputs and every other 16 rows each
     __syncwarp();
-    const int q = warp & 3, half = warp >> 2, n = n0 + 32 * q + lane;
+    const int q = warp & 3, half = warp >> 2, n = n0 + 32 * q + lane;   // half == 2: no part in it
     const uint32_t acc_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const bool ok = warp_wait(&acc_full, 0) && !abort_flag;
     tc_fence_after();
@@ -256,32 +285,39 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const uint64_t step = drop_step(ep.drop);
     const float bias = ep.bias && n < p.N ? ld_as_float(ep.bias, ep.bias_f32, n) : 0.0f;
     float *sums = reinterpret_cast<float *>(smem);            // [row][128], once every stage has been read (acc_full)
-    for (int m0 = 16 * half; m0 < p.rows; m0 += 32) {
-        uint32_t r[16];
-        tmem_ld16(acc_lane + m0, r);
-        tmem_ld_wait();
-        reg_fence<16>(r);
-        float v[16];
+    if (p.split == 1) {
+        for (int m0 = FW_EP * half; m0 < p.M && half < 2; m0 += 2 * FW_EP) {
+            uint32_t r[FW_EP];
+            tmem_ld4(acc_lane + m0, r);
+            tmem_ld_wait();
+            reg_fence<FW_EP>(r);
+            float v[FW_EP];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) v[t] = __uint_as_float(r[t]);
-        if (p.split > 1) {
+            for (int t = 0; t < FW_EP; ++t) v[t] = __uint_as_float(r[t]);
+            if (ok && n < p.N)
+                ep_column<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, p.N, p.M - m0, alpha, step, v, bias);
+            __syncwarp();
+        }
+    } else {
+        for (int m0 = 16 * half; m0 < p.M && half < 2; m0 += 32) {
+            uint32_t r[16];
+            tmem_ld16(acc_lane + m0, r);
+            tmem_ld_wait();
+            reg_fence<16>(r);
 #pragma unroll
-            for (int t = 0; t < 16; ++t) sums[(m0 + t) * FW_BN + 32 * q + lane] = v[t];
-        } else if (ok && n < p.N)
-            ep_column16<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, p.N, p.M - m0, alpha, step, v, bias);
-        __syncwarp();
-    }
-    if (p.split > 1) {
+            for (int t = 0; t < 16; ++t) sums[(m0 + t) * FW_BN + 32 * q + lane] = __uint_as_float(r[t]);
+        }
         cluster_sync();                                       // every CTA's sums are in its shared memory
-        // rows rank, rank + split, ..: 16 of them at a time, the two halves in turn
+        // rows rank, rank + split, ..: FW_EP of them at a time, the two halves in turn
         const uint32_t base = smem_u32(smem) + 4 * (32 * q + lane);
-        if (ok && n < p.N)
-            for (int m0 = rank + 16 * half * p.split; m0 < p.M; m0 += 32 * p.split) {
-                float v[16];
-                const int nm = imin(16, (p.M - m0 + p.split - 1) / p.split);
+        if (ok && n < p.N && half < 2)
+#pragma unroll 1
+            for (int m0 = rank + FW_EP * half * p.split; m0 < p.M; m0 += 2 * FW_EP * p.split) {
+                const int nm = imin(FW_EP, (p.M - m0 + p.split - 1) / p.split);
                 const uint32_t from = base + 4 * FW_BN * m0;
+                float v[FW_EP];
 #pragma unroll
-                for (int t = 0; t < 16; ++t) {
+                for (int t = 0; t < FW_EP; ++t) {
                     float x[FW_MAX_SPLIT];
 #pragma unroll
                     for (int r = 0; r < FW_MAX_SPLIT; ++r) {
@@ -292,8 +328,8 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
                     for (int r = 1; r < FW_MAX_SPLIT; ++r) v[t] += x[r];
                 }
-                ep_column16<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
-                                 alpha, step, v, bias);
+                ep_column<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
+                               alpha, step, v, bias);
             }
         __syncwarp();
         cluster_sync();                                       // nobody reads this CTA's shared memory any more
