@@ -574,14 +574,22 @@ def _step(step, index):
     return p
 
 
-def _new(shape, dtype, like, stream):
+def _new(like, stream, dtype, *shape):
     """A fresh tensor on `like`'s device, of the allocator's pool for the
     stream that the call runs on (its memory may still be in use elsewhere
     on any other)."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return _torch().empty(*shape, dtype=dtype, device=like.device)
     with _torch().cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return _torch().empty(*shape, dtype=dtype, device=like.device)
+
+
+def _new_like(like, stream):
+    """The same with `like`'s shape and type (contiguous, as `like` is)."""
+    if stream is None:
+        return _torch().empty_like(like)
+    with _torch().cuda.stream(stream):
+        return _torch().empty_like(like)
 
 
 def _call(fn, index, stream, *args):
@@ -610,7 +618,7 @@ def _scratch(workspace, nbytes, like, stream):
     if workspace is None:
         if not nbytes:
             return None, 0, None
-        workspace = _new((nbytes,), _torch().uint8, like, stream)
+        workspace = _new(like, stream, _torch().uint8, nbytes)
     return workspace.data_ptr(), workspace.nbytes, workspace
 
 
@@ -627,7 +635,7 @@ def _output(out, shape, out_dtype, like, index, stream):
     """(tensor, address, C type) of a bf16 or fp32 output."""
     torch = _torch()
     if out is None:
-        out = _new(shape, torch.float32 if out_dtype is None else out_dtype, like, stream)
+        out = _new(like, stream, torch.float32 if out_dtype is None else out_dtype, *shape)
         p = out.data_ptr()
     else:
         p = _tensor(out, "out", index, shape)
@@ -648,7 +656,7 @@ def _epilogue(shape, out, index, bias, act, want_preact, dropout_p, seed, step, 
         e.residual, e.residual_dt = _param(residual, "residual", index, shape)
     preact = None
     if want_preact is True:
-        preact = _new(shape, out.dtype, out, stream)
+        preact = _new_like(out, stream)
         e.preact = preact.data_ptr()
     elif want_preact is not False and want_preact is not None:
         preact = want_preact
@@ -713,10 +721,10 @@ def epilogue_backward(dY, Z=None, act=ACT_NONE, dropout_p=0.0, seed=0, step=None
     if out is not None:
         dZ, db = out.get("dZ"), out.get("dbias")
     if dZ is None:
-        dZ = _new(shape, dtype, dY, stream)
+        dZ = _new_like(dY, stream)
     pd = _tensor(dZ, "dZ", index, shape, dtype)
     if db is None and want_dbias:
-        db = _new((N,), _torch().float32, dY, stream)
+        db = _new(dY, stream, _torch().float32, N)
     if db is not None:
         pb = _tensor(db, "dbias", index, (N,), _torch().float32)
         ws, wsb, keep = _scratch(workspace, _epilogue_backward_ws(M, N), dY, stream)
@@ -734,7 +742,7 @@ def dropout(x, p, seed=0, step=None, residual=None, out=None, stream=None):
     dt = _xdt(x)
     pr = None if residual is None else _tensor(residual, "residual", index, x.shape, x.dtype)
     if out is None:
-        out = _new(x.shape, x.dtype, x, stream)
+        out = _new_like(x, stream)
         po = out.data_ptr()
     else:
         po = _tensor(out, "out", index, x.shape, x.dtype)
@@ -763,19 +771,19 @@ def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, want_stats=True, out=N
     pg, pb, wdt = _norm_params(index, D, gamma, beta)
     f32 = _torch().float32
     if out is None:
-        y = _new(shape, x.dtype, x, stream)
+        y = _new_like(x, stream)
         py, mean, rstd, pm, pr = y.data_ptr(), None, None, None, None
         if want_stats:
-            mean, rstd = _new((M,), f32, x, stream), _new((M,), f32, x, stream)
+            mean, rstd = _new(x, stream, f32, M), _new(x, stream, f32, M)
             pm, pr = mean.data_ptr(), rstd.data_ptr()
     else:
         y, mean, rstd = out.get("y"), out.get("mean"), out.get("rstd")
         if y is None:
-            y = _new(shape, x.dtype, x, stream)
+            y = _new_like(x, stream)
         if mean is None and want_stats:
-            mean = _new((M,), f32, x, stream)
+            mean = _new(x, stream, f32, M)
         if rstd is None and want_stats:
-            rstd = _new((M,), f32, x, stream)
+            rstd = _new(x, stream, f32, M)
         py = _tensor(y, "y", index, shape, x.dtype)
         pm = None if mean is None else _tensor(mean, "mean", index, (M,), f32)
         pr = None if rstd is None else _tensor(rstd, "rstd", index, (M,), f32)
@@ -800,11 +808,11 @@ def layernorm_backward(dy, x, gamma, mean, rstd, want_dx=True, want_dw=True, out
     if out is not None:
         dx, dg, db = out.get("dx"), out.get("dgamma"), out.get("dbeta")
     if dx is None and want_dx:
-        dx = _new(shape, dtype, x, stream)
+        dx = _new_like(x, stream)
     if dg is None and want_dw:
-        dg = _new((D,), f32, x, stream)
+        dg = _new(x, stream, f32, D)
     if db is None and want_dw:
-        db = _new((D,), f32, x, stream)
+        db = _new(x, stream, f32, D)
     px = None if dx is None else _tensor(dx, "dx", index, shape, dtype)
     pdg = None if dg is None else _tensor(dg, "dgamma", index, (D,), f32)
     pdb = None if db is None else _tensor(db, "dbeta", index, (D,), f32)

@@ -45,34 +45,34 @@ __device__ __forceinline__ float ld_dsmem(uint32_t cluster_addr)
 }
 
 // The epilogue of one column of the output, n (this thread's): element i0 + t
-// `stride` elements is row t of the nm rows (at most FW_EP) that exist.  Few
+// `stride` elements is row t of the nm rows (at most EP) that exist.  Few
 // rows at a time, so that the code stays short: with a row or two to finish,
 // fetching it is what the epilogue costs (sixteen at a time took 3 us more).
-constexpr int FW_EP = 4;
-template <int OUT>
+__host__ __device__ constexpr int fw_ep(int nx) { return nx == 1 ? 4 : 8; }
+template <int OUT, int EP>
 __device__ __forceinline__ void ep_column(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nm,
                                           float alpha, uint64_t step, const float *acc, float bias)
 {
-    float res[FW_EP], v[FW_EP];
+    float res[EP], v[EP];
     if (ep.residual)
 #pragma unroll
-        for (int t = 0; t < FW_EP; ++t)
+        for (int t = 0; t < EP; ++t)
             res[t] = t < nm ? ld_as_float(ep.residual, ep.residual_f32, i0 + t * stride) : 0.0f;
 #pragma unroll
-    for (int t = 0; t < FW_EP; ++t) v[t] = fmaf(acc[t], alpha, bias);
+    for (int t = 0; t < EP; ++t) v[t] = fmaf(acc[t], alpha, bias);
     auto store = [&](void *p) {
 #pragma unroll
-        for (int t = 0; t < FW_EP; ++t)
+        for (int t = 0; t < EP; ++t)
             if (t < nm) {
                 if (OUT == QFP4_F32) static_cast<float *>(p)[i0 + t * stride] = v[t];
                 else static_cast<__nv_bfloat16 *>(p)[i0 + t * stride] = __float2bfloat16_rn(v[t]);
             }
     };
     if (ep.preact) store(ep.preact);
-    act_forward<FW_EP>(v, ep.act);
+    act_forward<EP>(v, ep.act);
     if (ep.drop.on) {
 #pragma unroll
-        for (int t = 0; t < FW_EP; ++t) {
+        for (int t = 0; t < EP; ++t) {
             const uint64_t i = static_cast<uint64_t>(i0 + t * stride), q = i >> 2;
             const uint4 w = drop_words4(ep.drop, step, static_cast<uint32_t>(q), static_cast<uint32_t>(q >> 32));
             v[t] = drop1(ep.drop, v[t], i & 2 ? (i & 1 ? w.w : w.z) : (i & 1 ? w.y : w.x));
@@ -80,7 +80,7 @@ __device__ __forceinline__ void ep_column(const EpParams &ep, void *out, int64_t
     }
     if (ep.residual)
 #pragma unroll
-        for (int t = 0; t < FW_EP; ++t) v[t] += res[t];
+        for (int t = 0; t < EP; ++t) v[t] += res[t];
     store(out);
 }
 
@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     // ---------------------------------------------------- this CTA's sums: all
     // eight warps, a quadrant of outputs and every other 16 rows each
     __syncwarp();
+    constexpr int EP = fw_ep(NX);
     const int q = warp & 3, half = warp >> 2, n = n0 + 32 * q + lane;   // half == 2: no part in it
     const uint32_t acc_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const bool ok = warp_wait(&acc_full, 0) && !abort_flag;
@@ -286,16 +287,17 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const float bias = ep.bias && n < p.N ? ld_as_float(ep.bias, ep.bias_f32, n) : 0.0f;
     float *sums = reinterpret_cast<float *>(smem);            // [row][128], once every stage has been read (acc_full)
     if (p.split == 1) {
-        for (int m0 = FW_EP * half; m0 < p.M && half < 2; m0 += 2 * FW_EP) {
-            uint32_t r[FW_EP];
-            tmem_ld4(acc_lane + m0, r);
+        for (int m0 = EP * half; m0 < p.M && half < 2; m0 += 2 * EP) {
+            uint32_t r[EP];
+            if constexpr (EP == 4) tmem_ld4(acc_lane + m0, r);
+            else tmem_ld8(acc_lane + m0, r);
             tmem_ld_wait();
-            reg_fence<FW_EP>(r);
-            float v[FW_EP];
+            reg_fence<EP>(r);
+            float v[EP];
 #pragma unroll
-            for (int t = 0; t < FW_EP; ++t) v[t] = __uint_as_float(r[t]);
+            for (int t = 0; t < EP; ++t) v[t] = __uint_as_float(r[t]);
             if (ok && n < p.N)
-                ep_column<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, p.N, p.M - m0, alpha, step, v, bias);
+                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, p.N, p.M - m0, alpha, step, v, bias);
             __syncwarp();
         }
     } else {
@@ -308,16 +310,16 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
             for (int t = 0; t < 16; ++t) sums[(m0 + t) * FW_BN + 32 * q + lane] = __uint_as_float(r[t]);
         }
         cluster_sync();                                       // every CTA's sums are in its shared memory
-        // rows rank, rank + split, ..: FW_EP of them at a time, the two halves in turn
+        // rows rank, rank + split, ..: EP of them at a time, the two halves in turn
         const uint32_t base = smem_u32(smem) + 4 * (32 * q + lane);
         if (ok && n < p.N && half < 2)
 #pragma unroll 1
-            for (int m0 = rank + FW_EP * half * p.split; m0 < p.M; m0 += 2 * FW_EP * p.split) {
-                const int nm = imin(FW_EP, (p.M - m0 + p.split - 1) / p.split);
+            for (int m0 = rank + EP * half * p.split; m0 < p.M; m0 += 2 * EP * p.split) {
+                const int nm = imin(EP, (p.M - m0 + p.split - 1) / p.split);
                 const uint32_t from = base + 4 * FW_BN * m0;
-                float v[FW_EP];
+                float v[EP];
 #pragma unroll
-                for (int t = 0; t < FW_EP; ++t) {
+                for (int t = 0; t < EP; ++t) {
                     float x[FW_MAX_SPLIT];
 #pragma unroll
                     for (int r = 0; r < FW_MAX_SPLIT; ++r) {
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
                     for (int r = 1; r < FW_MAX_SPLIT; ++r) v[t] += x[r];
                 }
-                ep_column<OUT>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
+                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
                                alpha, step, v, bias);
             }
         __syncwarp();

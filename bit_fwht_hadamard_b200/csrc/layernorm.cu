@@ -168,9 +168,10 @@ static int launch_layernorm(const LnForward &a)
 // few rows that each has an SM to itself, as many threads as there are
 // vectors: the row's own latency is then all there is.
 constexpr int LN_ROWS = 4;
-template <int DT, int V>
-static int layernorm_by_size(const LnForward &a)
+template <int DT>
+static int layernorm_vectors(const LnForward &a)
 {
+    constexpr int V = ln_v<DT>();
     const int64_t nv = a.D / V;
     if (a.M <= 2 * 148) {
         if (nv <= 32) return launch_layernorm<DT, V, 32, 1, 1>(a);
@@ -189,12 +190,27 @@ static int layernorm_by_size(const LnForward &a)
     return launch_layernorm<DT, V, 1024, 4, 1>(a);
 }
 
+// Rows that do not start on 16 bytes, element by element.
+template <int DT>
+static int layernorm_elements(const LnForward &a)
+{
+    if (a.M <= 2 * 148) {
+        if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 1>(a);
+        if (a.D <= 8192) return launch_layernorm<DT, 1, 1024, 8, 1>(a);
+    }
+    if (a.D <= 256) return launch_layernorm<DT, 1, 32, 8, 2>(a);
+    if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 2>(a);
+    if (a.D <= 2048) return launch_layernorm<DT, 1, 256, 8, 2>(a);
+    if (a.D <= 4096) return launch_layernorm<DT, 1, 512, 8, 2>(a);
+    return launch_layernorm<DT, 1, 1024, 16, 1>(a);
+}
+
 template <int DT>
 static int layernorm_forward(const LnForward &a)
 {
     constexpr int V = ln_v<DT>();
-    if (a.D % V == 0 && a.D / V <= 4096) return layernorm_by_size<DT, V>(a);
-    if (a.D <= 4096) return layernorm_by_size<DT, 1>(a);
+    if (a.D % V == 0 && a.D / V <= 4096) return layernorm_vectors<DT>(a);
+    if (a.D <= 16384) return layernorm_elements<DT>(a);
     const int grid = static_cast<int>(imin<int64_t>(a.M, 16 * num_sms()));
     if (launch_pdl(k_layernorm_long<DT>, dim3(grid), dim3(1024), 0, a.s, a.x, a.M, a.D, a.gamma, a.beta, a.w32, a.eps,
                    a.y, a.mean, a.rstd) != cudaSuccess) {
@@ -551,15 +567,18 @@ static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
     const int vec = f32 ? 4 : 8;
     p.V = D % vec == 0 ? vec : 1;
     const int64_t nv = D / p.V;
-    if (nv <= 32) p.G = 32, p.NV = 1;
-    else if (nv <= 64) p.G = 32, p.NV = 2;
-    else if (p.V == 1) {
-        if (nv <= 128) p.G = 128, p.NV = 1;
-        else if (nv <= 512) p.G = 512, p.NV = 1;
-        else if (nv <= 1024) p.G = 1024, p.NV = 1;
-        else if (nv <= 2048) p.G = 1024, p.NV = 2;
-        else if (nv <= 4096) p.G = 1024, p.NV = 4;
-    } else if (nv <= 2048) {
+    if (p.V == 1) {
+        // element by element: eight of them a thread, for loads enough in flight
+        if (nv <= 256) p.G = 32, p.NV = 8;
+        else if (nv <= 1024) p.G = 128, p.NV = 8;
+        else if (nv <= 2048) p.G = 256, p.NV = 8;
+        else if (nv <= 4096) p.G = 512, p.NV = 8;
+        else if (nv <= 8192) p.G = 1024, p.NV = 8;
+    } else if (nv <= 32)
+        p.G = 32, p.NV = 1;
+    else if (nv <= 64)
+        p.G = 32, p.NV = 2;
+    else if (nv <= 2048) {
         // 512 threads an SM (1024 for the longest rows): one row of D = 4096
         // bf16 takes an SM's share of the memory rate about 1000 cycles, a
         // group's two passes over it about 700
@@ -627,15 +646,15 @@ static int launch_layernorm_ring(const LnBackward &a, const LnPlan &p)
 template <int DT, int V>
 static int layernorm_backward_by_size(const LnBackward &a, const LnPlan &p)
 {
-    if (p.G == 32)
-        return p.NV == 1 ? launch_layernorm_backward<DT, V, 32, 1>(a, p) : launch_layernorm_backward<DT, V, 32, 2>(a, p);
     if constexpr (V == 1) {
-        if (p.G == 128) return launch_layernorm_backward<DT, 1, 128, 1>(a, p);
-        if (p.G == 512) return launch_layernorm_backward<DT, 1, 512, 1>(a, p);
-        if (p.NV == 1) return launch_layernorm_backward<DT, 1, 1024, 1>(a, p);
-        if (p.NV == 2) return launch_layernorm_backward<DT, 1, 1024, 2>(a, p);
-        return launch_layernorm_backward<DT, 1, 1024, 4>(a, p);
+        if (p.G == 32) return launch_layernorm_backward<DT, 1, 32, 8>(a, p);
+        if (p.G == 128) return launch_layernorm_backward<DT, 1, 128, 8>(a, p);
+        if (p.G == 256) return launch_layernorm_backward<DT, 1, 256, 8>(a, p);
+        if (p.G == 512) return launch_layernorm_backward<DT, 1, 512, 8>(a, p);
+        return launch_layernorm_backward<DT, 1, 1024, 8>(a, p);
     } else {
+        if (p.G == 32)
+            return p.NV == 1 ? launch_layernorm_backward<DT, V, 32, 1>(a, p) : launch_layernorm_backward<DT, V, 32, 2>(a, p);
         if (p.G == 128) return launch_layernorm_ring<DT, 128, 1, 4>(a, p);
         if (p.G == 256)
             return p.NV == 1 ? launch_layernorm_ring<DT, 256, 1, 2>(a, p) : launch_layernorm_ring<DT, 256, 2, 2>(a, p);
