@@ -22,29 +22,96 @@ __host__ __device__ constexpr int ln_v()
     return DT == QFP4_F32 ? 4 : 8;
 }
 
+// ------------------------------------------------------------------ vectors at a row's ends
+// A vector of elements i .. i + V - 1 of a matrix of n, columns c .. c + V - 1
+// of a row of D: only the columns in [0, D) belong to the row; the others, a
+// neighbouring row's, become zeros.  Only a vector past the matrix's end goes
+// element by element.
+template <int DT, int V>
+__device__ __forceinline__ void ld_edge(Vec<DT, V> &v, const void *p, int64_t i, int64_t n, int c, int D)
+{
+    if (i + V <= n) {
+        v.load(p, i);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool out = c + j < 0 || c + j >= D;
+            if (DT == QFP4_F32) v.r[j % 4] = out ? 0u : v.r[j % 4];
+            else if (out) v.r[j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v.r[k] = 0u;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (c + j >= 0 && c + j < D) v.load1(p, i, j);
+}
+template <int DT, int V>
+__device__ __forceinline__ void st_edge(const Vec<DT, V> &v, void *p, int64_t i, int c, int D)
+{
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (c + j >= 0 && c + j < D) v.store1(p, i, j);
+}
+template <int V>
+__device__ __forceinline__ Fv<V> inside_row(const Fv<V> &f, int c, int D)
+{
+    float v[V];
+    f.to(v);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (c + j < 0 || c + j >= D) v[j] = 0.0f;
+    return Fv<V>::of(v);
+}
+// Parameters of columns c .. c + V - 1 (0 outside the row), c any column with SHIFT.
+template <int V, bool SHIFT>
+__device__ __forceinline__ Fv<V> ld_columns(const void *p, int f32, int c, int D)
+{
+    if constexpr (!SHIFT) return ld_param<V>(p, f32, c);
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = c + j >= 0 && c + j < D ? ld_as_float(p, f32, c + j) : 0.0f;
+    return Fv<V>::of(v);
+}
+
 // ------------------------------------------------------------------ forward
-// G threads take R rows at once, NV vectors of V elements of each: D <= G NV V.
-// The rows stay as they were loaded (unpacking them again for each of the
-// three steps is cheap); R rows share the reads of gamma and beta, which for
-// one row are as many bytes as the row itself and more, and the barriers.
-template <int DT, int V, int G, int NV, int R>
+// G threads take R rows at once, NV vectors of V elements of each.  The rows
+// stay as they were loaded (unpacking them again for each of the three steps
+// is cheap); R rows share the reads of gamma and beta, which for one row are
+// as many bytes as the row itself and more, and the barriers.
+//
+// V = 1: rows that do not start on 16 bytes, element by element.  SHIFT: such
+// rows, too long for that (a thread would hold too many elements, 4096 x 4098
+// bf16 106 us against 38).  Vectors are then aligned in memory, not in the row:
+// row m starts off = (m D) mod V elements into one, the same for rows V apart,
+// which are the R rows that a group takes; the vectors that straddle a row's
+// ends go element by element.
+template <int DT, int V, int G, int NV, int R, bool SHIFT>
 __global__ void __launch_bounds__(G == 32 ? 128 : G)
     k_layernorm(const void *x, int64_t M, int D, const void *gamma, const void *beta, int w32, float eps, void *y,
                 float *mean_out, float *rstd_out)
 {
+    constexpr int STEP = SHIFT ? V : 1;
     __shared__ float red[2][R][G == 32 ? 1 : G / 32];
     pdl_wait();
     pdl_trigger();
     const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t m = R * (G == 32 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x));
+    const int64_t gi = G == 32 ? blockIdx.x * 4ll + (threadIdx.x >> 5) : static_cast<int64_t>(blockIdx.x);
+    const int64_t m = SHIFT ? gi / V * (V * R) + gi % V : gi * R;
     if (m >= M) return;                                       // a whole group
-    const int nv = D / V;
+    const int off = SHIFT ? static_cast<int>(gi % V) * (D % V) % V : 0;
+    const int nv = SHIFT ? (D + off + V - 1) / V : D / V;
     Vec<DT, V> raw[R][NV];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-            if (t + k * G < nv && m + r < M) raw[r][k].load(x, (m + r) * D + static_cast<int64_t>(t + k * G) * V);
+            if (t + k * G < nv && m + r * STEP < M) {
+                const int c = (t + k * G) * V - off;
+                const int64_t i = (m + r * STEP) * D + c;
+                if (!SHIFT || (c >= 0 && c + V <= D)) raw[r][k].load(x, i);
+                else if constexpr (SHIFT) ld_edge(raw[r][k], x, i, M * D, c, D);
+            }
     const float inv = 1.0f / static_cast<float>(D);
     float mean[R], rstd[R];
 #pragma unroll
@@ -64,7 +131,10 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (t + k * G < nv) {
-                const Fv<V> d = raw[r][k].values() - mean2;
+                Fv<V> d = raw[r][k].values() - mean2;
+                const int c = (t + k * G) * V - off;
+                if constexpr (SHIFT)
+                    if (c < 0 || c + V > D) d = inside_row(d, c, D);
                 s = fma(d, d, s);
             }
         rstd[r] = s.sum();
@@ -75,22 +145,25 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
 #pragma unroll
     for (int k = 0; k < NV; ++k)
         if (t + k * G < nv) {
-            const int64_t c = static_cast<int64_t>(t + k * G) * V;
-            const Fv<V> g = gamma ? ld_param<V>(gamma, w32, c) : Fv<V>::splat(1.0f);
-            const Fv<V> b = beta ? ld_param<V>(beta, w32, c) : Fv<V>::splat(0.0f);
+            const int c = (t + k * G) * V - off;
+            const bool whole = !SHIFT || (c >= 0 && c + V <= D);
+            const Fv<V> g = gamma ? ld_columns<V, SHIFT>(gamma, w32, c, D) : Fv<V>::splat(1.0f);
+            const Fv<V> b = beta ? ld_columns<V, SHIFT>(beta, w32, c, D) : Fv<V>::splat(0.0f);
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                if (m + r < M) {
+                if (m + r * STEP < M) {
+                    const int64_t i = (m + r * STEP) * D + c;
                     raw[r][k].set(fma((raw[r][k].values() - Fv<V>::splat(mean[r])) * Fv<V>::splat(rstd[r]), g, b));
-                    raw[r][k].store(y, (m + r) * D + c);
+                    if (whole) raw[r][k].store(y, i);
+                    else if constexpr (SHIFT) st_edge(raw[r][k], y, i, c, D);
                 }
         }
     if (t == 0)
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            if (m + r < M) {
-                if (mean_out) mean_out[m + r] = mean[r];
-                if (rstd_out) rstd_out[m + r] = rstd[r];
+            if (m + r * STEP < M) {
+                if (mean_out) mean_out[m + r * STEP] = mean[r];
+                if (rstd_out) rstd_out[m + r * STEP] = rstd[r];
             }
 }
 
@@ -149,11 +222,11 @@ struct LnForward {
     cudaStream_t s;
 };
 
-template <int DT, int V, int G, int NV, int R>
+template <int DT, int V, int G, int NV, int R, bool SHIFT>
 static int launch_layernorm(const LnForward &a)
 {
-    const int64_t rows = (a.M + R - 1) / R;
-    if (launch_pdl(k_layernorm<DT, V, G, NV, R>, dim3(static_cast<unsigned>(G == 32 ? (rows + 3) / 4 : rows)),
+    const int64_t groups = SHIFT ? (a.M + V * R - 1) / (V * R) * V : (a.M + R - 1) / R;
+    if (launch_pdl(k_layernorm<DT, V, G, NV, R, SHIFT>, dim3(static_cast<unsigned>(G == 32 ? (groups + 3) / 4 : groups)),
                    dim3(G == 32 ? 128 : G), 0, a.s, a.x, a.M, static_cast<int>(a.D), a.gamma, a.beta, a.w32, a.eps, a.y,
                    a.mean, a.rstd) != cudaSuccess) {
         (void)cudaGetLastError();
@@ -163,10 +236,11 @@ static int launch_layernorm(const LnForward &a)
     return QFP4_OK;
 }
 
-// The group of a row: a warp up to 64 vectors; else four vectors a thread and
-// LN_ROWS rows at once, which keeps the most bytes in flight an SM.  With so
-// few rows that each has an SM to itself, as many threads as there are
-// vectors: the row's own latency is then all there is.
+// The group of a row: a warp up to 128 vectors; else four vectors a thread,
+// LN_ROWS rows at once, which keeps the most bytes in flight an SM (16384 x
+// 4096 bf16: 44 us; one row at once 55, two 44; 256 threads and two vectors
+// 50).  With so few rows that each has an SM to itself, as many threads as
+// there are vectors: the row's own latency is then all there is.
 constexpr int LN_ROWS = 4;
 template <int DT>
 static int layernorm_vectors(const LnForward &a)
@@ -174,35 +248,33 @@ static int layernorm_vectors(const LnForward &a)
     constexpr int V = ln_v<DT>();
     const int64_t nv = a.D / V;
     if (a.M <= 2 * 148) {
-        if (nv <= 32) return launch_layernorm<DT, V, 32, 1, 1>(a);
-        if (nv <= 128) return launch_layernorm<DT, V, 128, 1, 1>(a);
-        if (nv <= 512) return launch_layernorm<DT, V, 512, 1, 1>(a);
-        if (nv <= 1024) return launch_layernorm<DT, V, 1024, 1, 1>(a);
-        return launch_layernorm<DT, V, 1024, 4, 1>(a);
+        if (nv <= 32) return launch_layernorm<DT, V, 32, 1, 1, false>(a);
+        if (nv <= 128) return launch_layernorm<DT, V, 128, 1, 1, false>(a);
+        if (nv <= 512) return launch_layernorm<DT, V, 512, 1, 1, false>(a);
+        if (nv <= 1024) return launch_layernorm<DT, V, 1024, 1, 1, false>(a);
+        return launch_layernorm<DT, V, 1024, 4, 1, false>(a);
     }
-    if (nv <= 32) return launch_layernorm<DT, V, 32, 1, LN_ROWS>(a);
-    if (nv <= 64) return launch_layernorm<DT, V, 32, 2, LN_ROWS>(a);
-    if (nv <= 128) return launch_layernorm<DT, V, 32, 4, LN_ROWS>(a);
-    if (nv <= 256) return launch_layernorm<DT, V, 64, 4, LN_ROWS>(a);
-    if (nv <= 512) return launch_layernorm<DT, V, 128, 4, LN_ROWS>(a);
-    if (nv <= 1024) return launch_layernorm<DT, V, 256, 4, LN_ROWS>(a);
-    if (nv <= 2048) return launch_layernorm<DT, V, 512, 4, LN_ROWS>(a);
-    return launch_layernorm<DT, V, 1024, 4, 1>(a);
+    if (nv <= 32) return launch_layernorm<DT, V, 32, 1, LN_ROWS, false>(a);
+    if (nv <= 64) return launch_layernorm<DT, V, 32, 2, LN_ROWS, false>(a);
+    if (nv <= 128) return launch_layernorm<DT, V, 32, 4, LN_ROWS, false>(a);
+    if (nv <= 256) return launch_layernorm<DT, V, 64, 4, LN_ROWS, false>(a);
+    if (nv <= 512) return launch_layernorm<DT, V, 128, 4, LN_ROWS, false>(a);
+    if (nv <= 1024) return launch_layernorm<DT, V, 256, 4, LN_ROWS, false>(a);
+    if (nv <= 2048) return launch_layernorm<DT, V, 512, 4, LN_ROWS, false>(a);
+    return launch_layernorm<DT, V, 1024, 4, 1, false>(a);
 }
 
-// Rows that do not start on 16 bytes, element by element.
 template <int DT>
 static int layernorm_elements(const LnForward &a)
 {
     if (a.M <= 2 * 148) {
-        if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 1>(a);
-        if (a.D <= 8192) return launch_layernorm<DT, 1, 1024, 8, 1>(a);
+        if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 1, false>(a);
+        return launch_layernorm<DT, 1, 1024, 4, 1, false>(a);
     }
-    if (a.D <= 256) return launch_layernorm<DT, 1, 32, 8, 2>(a);
-    if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 2>(a);
-    if (a.D <= 2048) return launch_layernorm<DT, 1, 256, 8, 2>(a);
-    if (a.D <= 4096) return launch_layernorm<DT, 1, 512, 8, 2>(a);
-    return launch_layernorm<DT, 1, 1024, 16, 1>(a);
+    if (a.D <= 256) return launch_layernorm<DT, 1, 32, 8, 2, false>(a);
+    if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 2, false>(a);
+    if (a.D <= 2048) return launch_layernorm<DT, 1, 256, 8, 2, false>(a);
+    return launch_layernorm<DT, 1, 512, 8, 2, false>(a);
 }
 
 template <int DT>
@@ -210,7 +282,10 @@ static int layernorm_forward(const LnForward &a)
 {
     constexpr int V = ln_v<DT>();
     if (a.D % V == 0 && a.D / V <= 4096) return layernorm_vectors<DT>(a);
-    if (a.D <= 16384) return layernorm_elements<DT>(a);
+    if (a.D % V != 0 && a.D <= 4096) return layernorm_elements<DT>(a);
+    const int64_t nv = (a.D + 2 * (V - 1)) / V;               // at most, whatever the row's offset
+    if (a.D % V != 0 && nv <= 1024) return launch_layernorm<DT, V, 256, 4, LN_ROWS, true>(a);
+    if (a.D % V != 0 && nv <= 2048) return launch_layernorm<DT, V, 512, 4, LN_ROWS, true>(a);
     const int grid = static_cast<int>(imin<int64_t>(a.M, 16 * num_sms()));
     if (launch_pdl(k_layernorm_long<DT>, dim3(grid), dim3(1024), 0, a.s, a.x, a.M, a.D, a.gamma, a.beta, a.w32, a.eps,
                    a.y, a.mean, a.rstd) != cudaSuccess) {
@@ -222,22 +297,54 @@ static int layernorm_forward(const LnForward &a)
 }
 
 // ------------------------------------------------------------------ backward
-// One pass: a group of G threads takes a row of every gridDim.x-th group,
-// NV vectors a thread; the next row's loads are issued before the row sums of
-// the present one are joined.  A thread keeps the sums of dy xhat and dy of
-// its own columns in registers over all its rows; at the end each block
-// writes them as one row of the partial sums (the four warps of a block with
-// G = 32 joined first).
-template <int DT, int V, int G, int NV>
-__global__ void __launch_bounds__(G == 32 ? 128 : G)
+// The column sums of a block's GR groups, one group after the other, added to
+// the first's.  buf: G NV V floats.
+template <int G, int NV, int GR, int V>
+__device__ __forceinline__ void join_groups(Fv<V> *v, float *buf, int gi, int t)
+{
+#pragma unroll
+    for (int from = 1; from < GR; ++from) {
+        __syncthreads();
+        if (gi == from) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float o[V];
+                v[k].to(o);
+#pragma unroll
+                for (int j = 0; j < V; ++j) buf[(k * V + j) * G + t] = o[j];
+            }
+        }
+        __syncthreads();
+        if (gi == 0) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float o[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) o[j] = buf[(k * V + j) * G + t];
+                v[k] = v[k] + Fv<V>::of(o);
+            }
+        }
+    }
+}
+
+// One pass: a group of G threads takes every groups-th row, NV vectors a
+// thread; the next row's loads are issued before the row sums of the present
+// one are joined.  A thread keeps the sums of dy xhat and dy of its own columns
+// in registers over all its rows; at the end each block joins its GR groups'
+// sums and writes them as one row of the partial sums.  V = 1: rows that do not
+// start on 16 bytes, element by element.
+template <int DT, int V, int G, int NV, int GR>
+__global__ void __launch_bounds__(GR *G)
     k_layernorm_backward(const void *dy, const void *x, int64_t M, int D, const void *gamma, int w32,
                          const float *mean_in, const float *rstd_in, void *dx, float *partial)
 {
-    __shared__ float2 red[2][G == 32 ? 1 : G / 32];
-    __shared__ float join[G == 32 ? 3 : 1][G == 32 ? 32 * NV * V : 1];
+    __shared__ float2 red[GR][2][G / 32];
+    __shared__ float join[GR > 1 ? G * NV * V : 1];
     pdl_wait();
     pdl_trigger();
-    const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x, wg = G == 32 ? threadIdx.x >> 5 : 0;
+    const int t = threadIdx.x % G, gi = threadIdx.x / G;
+    const int64_t groups = static_cast<int64_t>(gridDim.x) * GR;
+    int64_t m = static_cast<int64_t>(gi) * gridDim.x + blockIdx.x;
     const int nv = D / V;
     const float inv = 1.0f / static_cast<float>(D);
     Fv<V> sg[NV], sb[NV], w[NV];
@@ -245,10 +352,8 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
     for (int k = 0; k < NV; ++k) {
         sg[k] = sb[k] = Fv<V>::splat(0.0f);
         w[k] = Fv<V>::splat(1.0f);
-        if (gamma && t + k * G < nv) w[k] = ld_param<V>(gamma, w32, static_cast<int64_t>(t + k * G) * V);
+        if (gamma && t + k * G < nv) w[k] = ld_param<V>(gamma, w32, (t + k * G) * V);
     }
-    const int64_t groups = G == 32 ? gridDim.x * 4ll : gridDim.x;
-    int64_t m = G == 32 ? blockIdx.x * 4ll + wg : blockIdx.x;
     Vec<DT, V> rd[NV], rx[NV];
     float mean = 0.0f, rstd = 0.0f;
     auto load = [&](int64_t row) {
@@ -257,7 +362,7 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (t + k * G < nv) {
-                const int64_t i = row * D + static_cast<int64_t>(t + k * G) * V;
+                const int64_t i = row * D + (t + k * G) * V;
                 rd[k].load(dy, i);
                 rx[k].load(x, i);
             }
@@ -280,50 +385,33 @@ __global__ void __launch_bounds__(G == 32 ? 128 : G)
         }
         if (m + groups < M) load(m + groups);
         if (!dx) continue;
-        const float2 c = group_sum2<G>(s1.sum(), s2.sum(), red[par], 1);
+        const float2 c = group_sum2<G>(s1.sum(), s2.sum(), red[gi][par], 1 + gi);
         const Fv<V> c1 = Fv<V>::splat(c.x * inv), c2 = Fv<V>::splat(c.y * inv);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (t + k * G < nv) {
                 Vec<DT, V> o;
                 o.set(rstd2 * (g[k] - fma(xh[k], c2, c1)));
-                o.store(dx, m * D + static_cast<int64_t>(t + k * G) * V);
+                o.store(dx, m * D + (t + k * G) * V);
             }
     }
     if (!partial) return;
-    float *pg = partial + static_cast<int64_t>(blockIdx.x) * D;
-    float *pb = pg + static_cast<int64_t>(gridDim.x) * D;
-    float vg[NV * V], vb[NV * V];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        sg[k].to(vg + k * V);
-        sb[k].to(vb + k * V);
-    }
-    if constexpr (G == 32) {
+    for (int half = 0; half < 2; ++half) {
+        Fv<V> *v = half ? sb : sg;
+        join_groups<G, NV, GR, V>(v, join, gi, t);
+        if (gi == 0) {
+            float *dst = partial + (half * static_cast<int64_t>(gridDim.x) + blockIdx.x) * D;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float *v = half ? vb : vg;
-            __syncthreads();
-            if (wg > 0)
+            for (int k = 0; k < NV; ++k)
+                if (t + k * G < nv) {
+                    float o[V];
+                    v[k].to(o);
 #pragma unroll
-                for (int k = 0; k < NV * V; ++k) join[wg - 1][k * 32 + t] = v[k];
-            __syncthreads();
-            if (wg == 0)
-#pragma unroll
-                for (int k = 0; k < NV * V; ++k)
-                    v[k] = (v[k] + join[0][k * 32 + t]) + (join[1][k * 32 + t] + join[2][k * 32 + t]);
+                    for (int j = 0; j < V; ++j) dst[(t + k * G) * V + j] = o[j];
+                }
         }
-        if (wg > 0) return;
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-        if (t + k * G < nv)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int64_t c = static_cast<int64_t>(t + k * G) * V + j;
-                pg[c] = vg[k * V + j];
-                pb[c] = vb[k * V + j];
-            }
 }
 
 // Aligned rows of 65 to 2048 vectors (bf16 D in (512, 16384], binary32 D in
@@ -436,45 +524,11 @@ __global__ void __launch_bounds__(GR *G, 1)
     if (!ok) settle_ns(kSettleNs);                            // copies already issued may still be landing
     __syncthreads();
     if (!partial) return;
-    // the other groups' sums, one group after the other, through shared memory
-    // (no copy is under way now) to the first
-    float *join = reinterpret_cast<float *>(ln_smem);
+    // (no copy is under way now: the ring's memory is free)
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         Fv<V> *v = half ? sb : sg;
-#pragma unroll
-        for (int from = 1; from < GR; ++from) {
-            if (gi == from) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    if (t + k * G < nv) {
-                        float o[V];
-                        v[k].to(o);
-#pragma unroll
-                        for (int j = 0; j < V; j += 4)
-                            *reinterpret_cast<float4 *>(join + (t + k * G) * V + j) =
-                                make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                    }
-            }
-            __syncthreads();
-            if (gi == 0) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    if (t + k * G < nv) {
-                        float o[V];
-#pragma unroll
-                        for (int j = 0; j < V; j += 4) {
-                            const float4 u = *reinterpret_cast<const float4 *>(join + (t + k * G) * V + j);
-                            o[j] = u.x;
-                            o[j + 1] = u.y;
-                            o[j + 2] = u.z;
-                            o[j + 3] = u.w;
-                        }
-                        v[k] = v[k] + Fv<V>::of(o);
-                    }
-            }
-            __syncthreads();
-        }
+        join_groups<G, NV, GR, V>(v, reinterpret_cast<float *>(ln_smem), gi, t);
         if (gi == 0) {
             float *dst = partial + (half * static_cast<int64_t>(gridDim.x) + blockIdx.x) * D;
 #pragma unroll
@@ -492,7 +546,7 @@ __global__ void __launch_bounds__(GR *G, 1)
 }
 
 // Rows too long for that: the column sums and dx in a kernel each.
-template <int DT>
+template <int DT, int V>
 __global__ void __launch_bounds__(1024) k_layernorm_dx_long(const void *dy, const void *x, int64_t M, int64_t D,
                                                              const void *gamma, int w32, const float *mean_in,
                                                              const float *rstd_in, void *dx)
@@ -504,26 +558,34 @@ __global__ void __launch_bounds__(1024) k_layernorm_dx_long(const void *dy, cons
     int par = 0;
     for (int64_t m = blockIdx.x; m < M; m += gridDim.x, par ^= 1) {
         const int64_t r = m * D;
-        const float mean = mean_in[m], rstd = rstd_in[m];
-        float s1[4] = {}, s2[4] = {};
-        for (int64_t c = threadIdx.x; c < D; c += 4096)
+        const Fv<V> mean = Fv<V>::splat(mean_in[m]), rstd = Fv<V>::splat(rstd_in[m]);
+        auto terms = [&](int64_t c, Fv<V> &g, Fv<V> &h) {
+            Vec<DT, V> a, b;
+            a.load(dy, r + c);
+            b.load(x, r + c);
+            g = a.values();
+            if (gamma) g = g * ld_param<V>(gamma, w32, c);
+            h = (b.values() - mean) * rstd;
+        };
+        Fv<V> s1[2], s2[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + 1024 * j < D) {
-                    float g = ld_as_float(dy, DT == QFP4_F32, r + c + 1024 * j);
-                    if (gamma) g *= ld_as_float(gamma, w32, c + 1024 * j);
-                    s1[j] += g;
-                    s2[j] = fmaf(g, (ld_as_float(x, DT == QFP4_F32, r + c + 1024 * j) - mean) * rstd, s2[j]);
+        for (int j = 0; j < 2; ++j) s1[j] = s2[j] = Fv<V>::splat(0.0f);
+        for (int64_t c = threadIdx.x * V; c < D; c += 2048 * V)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (c + 1024 * V * j < D) {
+                    Fv<V> g, h;
+                    terms(c + 1024 * V * j, g, h);
+                    s1[j] = s1[j] + g;
+                    s2[j] = fma(g, h, s2[j]);
                 }
-        const float2 t = group_sum2<1024>((s1[0] + s1[1]) + (s1[2] + s1[3]), (s2[0] + s2[1]) + (s2[2] + s2[3]),
-                                          red[par], 1);
-        const float c1 = t.x * inv, c2 = t.y * inv;
-        for (int64_t c = threadIdx.x; c < D; c += 1024) {
-            float g = ld_as_float(dy, DT == QFP4_F32, r + c);
-            if (gamma) g *= ld_as_float(gamma, w32, c);
-            const float v = rstd * (g - fmaf((ld_as_float(x, DT == QFP4_F32, r + c) - mean) * rstd, c2, c1));
-            Vec<DT, 1> o;
-            o.set(&v);
+        const float2 t = group_sum2<1024>((s1[0] + s1[1]).sum(), (s2[0] + s2[1]).sum(), red[par], 1);
+        const Fv<V> c1 = Fv<V>::splat(t.x * inv), c2 = Fv<V>::splat(t.y * inv);
+        for (int64_t c = threadIdx.x * V; c < D; c += 1024 * V) {
+            Fv<V> g, h;
+            terms(c, g, h);
+            Vec<DT, V> o;
+            o.set(rstd * (g - fma(h, c2, c1)));
             o.store(dx, r + c);
         }
     }
@@ -565,36 +627,39 @@ static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
 {
     LnPlan p{};
     const int vec = f32 ? 4 : 8;
-    p.V = D % vec == 0 ? vec : 1;
+    p.V = D % vec ? 1 : vec;
     const int64_t nv = D / p.V;
+    p.GR = 1;
     if (p.V == 1) {
-        // element by element: eight of them a thread, for loads enough in flight
-        if (nv <= 256) p.G = 32, p.NV = 8;
-        else if (nv <= 1024) p.G = 128, p.NV = 8;
-        else if (nv <= 2048) p.G = 256, p.NV = 8;
-        else if (nv <= 4096) p.G = 512, p.NV = 8;
-        else if (nv <= 8192) p.G = 1024, p.NV = 8;
+        // eight elements a thread, for loads enough in flight (16384 x 1001
+        // bf16: 39 us; one element a thread 232)
+        p.NV = 8;
+        if (nv <= 256) p.G = 32, p.GR = 4;
+        else if (nv <= 1024) p.G = 128;
+        else if (nv <= 2048) p.G = 256;
+        else if (nv <= 4096) p.G = 512;
+        else if (nv <= 8192) p.G = 1024;
     } else if (nv <= 32)
-        p.G = 32, p.NV = 1;
+        p.G = 32, p.NV = 1, p.GR = 4;
     else if (nv <= 64)
-        p.G = 32, p.NV = 2;
+        p.G = 32, p.NV = 2, p.GR = 4;
     else if (nv <= 2048) {
         // 512 threads an SM (1024 for the longest rows): one row of D = 4096
         // bf16 takes an SM's share of the memory rate about 1000 cycles, a
         // group's two passes over it about 700
-        if (nv <= 128) p.G = 128, p.NV = 1, p.GR = 4;
-        else if (nv <= 256) p.G = 256, p.NV = 1, p.GR = 2;
-        else if (nv <= 512) p.G = 256, p.NV = 2, p.GR = 2;
-        else if (nv <= 1024) p.G = 512, p.NV = 2, p.GR = 1;
-        else p.G = 1024, p.NV = 2, p.GR = 1;
+        p.NV = 2;
+        if (nv <= 128) p.G = 64, p.GR = 8;
+        else if (nv <= 256) p.G = 128, p.GR = 4;
+        else if (nv <= 512) p.G = 256, p.GR = 2;
+        else if (nv <= 1024) p.G = 512;
+        else p.G = 1024;
         p.stages = static_cast<int>(imin<int64_t>(8, LNB_SMEM / (p.GR * 2 * D * (f32 ? 4 : 2))));
     }
     if (p.stages) {
         p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, 148);
     } else if (p.G) {
         // blocks for 1024 threads an SM, but no more than there are rows
-        const int64_t per = p.G == 32 ? 4 : 1, threads = p.G == 32 ? 128 : p.G;
-        p.parts = imin<int64_t>((M + per - 1) / per, 148 * imax<int64_t>(1, 1024 / threads));
+        p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, 148 * (1024 / (p.G * p.GR)));
     } else {
         const int64_t cols = (D + 255) / 256;
         const int64_t want = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));
@@ -615,12 +680,12 @@ struct LnBackward {
     cudaStream_t s;
 };
 
-template <int DT, int V, int G, int NV>
+template <int DT, int V, int G, int NV, int GR>
 static int launch_layernorm_backward(const LnBackward &a, const LnPlan &p)
 {
-    if (launch_pdl(k_layernorm_backward<DT, V, G, NV>, dim3(static_cast<unsigned>(p.parts)),
-                   dim3(G == 32 ? 128 : G), 0, a.s, a.dy, a.x, a.M, static_cast<int>(a.D), a.gamma, a.w32, a.mean,
-                   a.rstd, a.dx, a.partial) != cudaSuccess) {
+    if (launch_pdl(k_layernorm_backward<DT, V, G, NV, GR>, dim3(static_cast<unsigned>(p.parts)), dim3(GR * G), 0,
+                   a.s, a.dy, a.x, a.M, static_cast<int>(a.D), a.gamma, a.w32, a.mean, a.rstd, a.dx,
+                   a.partial) != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
@@ -643,32 +708,31 @@ static int launch_layernorm_ring(const LnBackward &a, const LnPlan &p)
     return QFP4_OK;
 }
 
-template <int DT, int V>
+template <int DT>
 static int layernorm_backward_by_size(const LnBackward &a, const LnPlan &p)
 {
-    if constexpr (V == 1) {
-        if (p.G == 32) return launch_layernorm_backward<DT, 1, 32, 8>(a, p);
-        if (p.G == 128) return launch_layernorm_backward<DT, 1, 128, 8>(a, p);
-        if (p.G == 256) return launch_layernorm_backward<DT, 1, 256, 8>(a, p);
-        if (p.G == 512) return launch_layernorm_backward<DT, 1, 512, 8>(a, p);
-        return launch_layernorm_backward<DT, 1, 1024, 8>(a, p);
-    } else {
-        if (p.G == 32)
-            return p.NV == 1 ? launch_layernorm_backward<DT, V, 32, 1>(a, p) : launch_layernorm_backward<DT, V, 32, 2>(a, p);
-        if (p.G == 128) return launch_layernorm_ring<DT, 128, 1, 4>(a, p);
-        if (p.G == 256)
-            return p.NV == 1 ? launch_layernorm_ring<DT, 256, 1, 2>(a, p) : launch_layernorm_ring<DT, 256, 2, 2>(a, p);
-        if (p.G == 512) return launch_layernorm_ring<DT, 512, 2, 1>(a, p);
-        return launch_layernorm_ring<DT, 1024, 2, 1, false>(a, p);
+    if (p.V == 1) {
+        if (p.G == 32) return launch_layernorm_backward<DT, 1, 32, 8, 4>(a, p);
+        if (p.G == 128) return launch_layernorm_backward<DT, 1, 128, 8, 1>(a, p);
+        if (p.G == 256) return launch_layernorm_backward<DT, 1, 256, 8, 1>(a, p);
+        if (p.G == 512) return launch_layernorm_backward<DT, 1, 512, 8, 1>(a, p);
+        return launch_layernorm_backward<DT, 1, 1024, 8, 1>(a, p);
     }
+    if (p.G == 32)
+        return p.NV == 1 ? launch_layernorm_backward<DT, ln_v<DT>(), 32, 1, 4>(a, p)
+                         : launch_layernorm_backward<DT, ln_v<DT>(), 32, 2, 4>(a, p);
+    if (p.G == 64) return launch_layernorm_ring<DT, 64, 2, 8>(a, p);
+    if (p.G == 128) return launch_layernorm_ring<DT, 128, 2, 4>(a, p);
+    if (p.G == 256) return launch_layernorm_ring<DT, 256, 2, 2>(a, p);
+    if (p.G == 512) return launch_layernorm_ring<DT, 512, 2, 1>(a, p);
+    return launch_layernorm_ring<DT, 1024, 2, 1, false>(a, p);
 }
 
 template <int DT>
 static int layernorm_backward(const LnBackward &a, const LnPlan &p, float *dgamma, float *dbeta)
 {
     if (p.G) {
-        const int st = p.V == 1 ? layernorm_backward_by_size<DT, 1>(a, p)
-                                : layernorm_backward_by_size<DT, ln_v<DT>()>(a, p);
+        const int st = layernorm_backward_by_size<DT>(a, p);
         if (st != QFP4_OK || !a.partial) return st;
         return column_sums(a.partial, p.parts, a.D, static_cast<int>(a.D), 0, 1, dgamma, dbeta, true, a.s);
     }
@@ -685,8 +749,13 @@ static int layernorm_backward(const LnBackward &a, const LnPlan &p, float *dgamm
     }
     if (!a.dx) return QFP4_OK;
     const int grid = static_cast<int>(imin<int64_t>(a.M, 16 * num_sms()));
-    if (launch_pdl(k_layernorm_dx_long<DT>, dim3(grid), dim3(1024), 0, a.s, a.dy, a.x, a.M, a.D, a.gamma, a.w32, a.mean,
-                   a.rstd, a.dx) != cudaSuccess) {
+    const bool vectors = a.D % ln_v<DT>() == 0;
+    const cudaError_t e =
+        vectors ? launch_pdl(k_layernorm_dx_long<DT, ln_v<DT>()>, dim3(grid), dim3(1024), 0, a.s, a.dy, a.x, a.M, a.D,
+                             a.gamma, a.w32, a.mean, a.rstd, a.dx)
+                : launch_pdl(k_layernorm_dx_long<DT, 1>, dim3(grid), dim3(1024), 0, a.s, a.dy, a.x, a.M, a.D, a.gamma,
+                             a.w32, a.mean, a.rstd, a.dx);
+    if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
