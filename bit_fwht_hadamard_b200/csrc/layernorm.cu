@@ -87,7 +87,7 @@ __device__ __forceinline__ Fv<V> ld_columns(const void *p, int f32, int c, int D
 // which are the R rows that a group takes; the vectors that straddle a row's
 // ends go element by element.
 template <int DT, int V, int G, int NV, int R, bool SHIFT>
-__global__ void __launch_bounds__(G == 32 ? 128 : G)
+__global__ void __launch_bounds__(G == 32 ? 128 : G, V == 8 && R == 4 && (G == 128 || (G == 32 && NV == 4)) ? 5 : 0)
     k_layernorm(const void *x, int64_t M, int D, const void *gamma, const void *beta, int w32, float eps, void *y,
                 float *mean_out, float *rstd_out)
 {
@@ -472,10 +472,9 @@ __global__ void __launch_bounds__(GR *G, 1)
             mean_next = mean_in[m + groups];
             rstd_next = rstd_in[m + groups];
         }
-        if (!mbar_wait(&full[s], phase)) {
-            ok = false;
-            break;
-        }
+        // after a wait that gave up (the error is recorded) the rows go on
+        // without waiting, so that every thread still meets the barriers
+        ok = ok && mbar_wait(&full[s], phase);
         const uint8_t *pd = ring + static_cast<size_t>(2 * s) * row_bytes, *px = pd + row_bytes;
         Fv<V> xh[KEEP ? NV : 1], g[KEEP ? NV : 1], s1 = Fv<V>::splat(0.0f), s2 = Fv<V>::splat(0.0f);
         const Fv<V> mean2 = Fv<V>::splat(mean), rstd2 = Fv<V>::splat(rstd);

@@ -383,7 +383,7 @@ int qfp4_linear_backward(const void *G, const void *X, const void *W, int64_t M,
  *   bias       N values of type bias_dt, or NULL.
  *   act        a qfp4_act.
  *   preact     out, M x N of the call's output type, or NULL: z, as
- *              qfp4_epilogue_backward needs it.  Must not overlap out.
+ *              qfp4_epilogue_backward needs it.  Must not overlap out or residual.
  *   dropout_p, seed, step   as in qfp4_dropout, with e = m*N + n; 0 <= p < 1.
  *   residual   M x N of type residual_dt, or NULL.  May be the out buffer
  *              itself where residual_dt is the output type.

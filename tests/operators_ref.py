@@ -115,3 +115,12 @@ def random_operand(rows, K, fmt, seed, device="cuda", spread=3):
     if fmt == 1:
         out["tscale"] = torch.tensor([0.0371], device=device)
     return out
+
+
+def keep_range(start, count, p, seed, step=0):
+    """keep() of elements start .. start + count - 1 (start a multiple of 4)."""
+    q = np.arange(start // 4, (start + count + 3) // 4, dtype=np.uint64)
+    c = [q & np.uint64(0xFFFFFFFF), q >> np.uint64(32), np.full_like(q, step & 0xFFFFFFFF),
+         np.full_like(q, (step >> 32) + (1 << 31))]
+    w = np.stack(philox(c, (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF)), -1).reshape(-1)[:count]
+    return w >= np.uint64(int(p * 2.0 ** 32))

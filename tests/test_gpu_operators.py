@@ -628,3 +628,68 @@ def test_a_transformer_block_forward_and_backward():
     inside(dx, rx, 3 * e * (rx.abs() + gy.double().abs()) + 2.0 ** -15 * rr[:, None], "dx")
     assert dW1.shape == W1.shape and dW2.shape == W2.shape
     assert all(bool(torch.isfinite(t).all()) for t in (dW1, dW2, db1, db2))
+
+
+# ------------------------------------------------------------------ offsets past 31 and 32 bits
+def test_dropout_past_32_bits():
+    """2^32 + 12 elements: every index in 64 bits, the counters' low words up to 2^30."""
+    n = (1 << 32) + 12
+    x = torch.ones((n,), dtype=BF, device="cuda")
+    y = q.dropout(x, 0.5, seed=4, step=step_of(3))
+    for start in (0, (1 << 31) - 8, (1 << 32) - 8):
+        k = torch.from_numpy(R.keep_range(start, 20, 0.5, 4, 3)).cuda()
+        assert torch.equal(y[start:start + 20] == 2, k) and torch.equal(y[start:start + 20] == 0, ~k)
+    kept = sum(int((c == 2).sum()) for c in y.split(1 << 28))
+    assert abs(kept - n / 2) < 6 * (n / 4) ** 0.5             # six standard deviations
+
+
+@pytest.mark.parametrize("D", [2056, 2051])
+def test_row_operators_past_31_bits(D):
+    """More than 2^31 elements: the last rows equal the same rows alone."""
+    M = (1 << 31) // D + 9
+    tail = normal((16, D), 1, dt=BF)
+    x = torch.empty((M, D), dtype=BF, device="cuda")
+    x[:-16].fill_(0.25)
+    x[-16:] = tail
+    g = 1 + normal((D,), 2, 0.3)
+    y, mean, rstd = q.layernorm_forward(x, g)
+    wy, wm, wr = R.layernorm(tail.double(), g.double(), None, float(np.float32(1e-5)))
+    inside(y[-16:], wy, 2.0 ** -8 * wy.abs() + 2.0 ** -16, "y")
+    inside(mean[-16:], wm, torch.full_like(wm, 2.0 ** -16), "mean")
+    del y
+    dx, dg, db = q.layernorm_backward(x, x, g, mean, rstd)
+    # the constant rows have xhat = 0 to rounding (their rstd is 1e-5^-1/2)
+    wx, wg, wb = R.layernorm_grads(tail.double(), tail.double(), g.double(), mean[-16:].double(), rstd[-16:].double())
+    inside(dx[-16:], wx, 2.0 ** -8 * wx.abs() + 2.0 ** -14, "dx")
+    inside(db, wb + 0.25 * (M - 16), torch.full_like(wb, M * U * 0.25 * M), "dbeta")
+    del dx
+    dz, dbias = q.epilogue_backward(x, x, act=q.ACT_SILU, dropout_p=0.5, seed=3)
+    first = (M - 16) * D // 4 * 4
+    k = torch.from_numpy(R.keep_range(first, M * D - first, 0.5, 3)).cuda()[(M - 16) * D - first:].view(16, D)
+    want = torch.where(k, 2 * tail.double() * R.slope(tail.double(), "silu"), torch.zeros((16, D), device="cuda").double())
+    inside(dz[-16:], want, 2.0 ** -8 * want.abs() + 2.0 ** -18 * tail.double().abs(), "dz")
+
+
+def test_gemm_epilogue_past_31_bits():
+    """An output of more than 2^31 elements: its last rows equal a small call's."""
+    M, N, K = 65552, 32776, 32
+    A, B = R.random_operand(M, K, q.MXFP4, 1), R.random_operand(N, K, q.MXFP4, 2)
+    y, _ = q.gemm_epilogue(A, B, M, N, K, q.MXFP4, act=q.ACT_RELU, out_dtype=BF)
+    t = {k: v[-200:].clone() for k, v in A.items()}
+    want, _ = q.gemm_epilogue(t, B, 200, N, K, q.MXFP4, act=q.ACT_RELU, out_dtype=BF)
+    assert torch.equal(y[-200:], want)                        # sums of one k-tile are exact
+
+
+def test_layernorm_ring_of_many_rows_is_the_same_again():
+    """Rows through the copies' ring many times over: the same bits each time."""
+    for M, D, dt in ((5000, 4096, BF), (3001, 1024, BF), (2000, 8192, F32), (999, 16384, BF)):
+        x, dy = norm_input(M, D, dt), normal((M, D), 2, dt=dt)
+        g = 1 + normal((D,), 3, 0.3)
+        _, mean, rstd = q.layernorm_forward(x, g)
+        first = q.layernorm_backward(dy, x, g, mean, rstd)
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(first, q.layernorm_backward(dy, x, g, mean, rstd)))
+        wx, wg, wb = R.layernorm_grads(dy.double(), x.double(), g.double(), mean.double(), rstd.double())
+        assert float((first[1].double() - wg).norm() / wg.norm()) < 1e-6
+        assert float((first[2].double() - wb).norm() / wb.norm()) < 1e-6
+    assert q.qfp4_last_device_error() == 0
