@@ -1224,7 +1224,7 @@ int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *
         QFP4_LAUNCH_CHECK();
         return QFP4_OK;
     }
-    if (M <= FW_ROWS)
+    if (gemm_few_fits(M, N))
         return gemm_few(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, ep, out_dt, out, stream);
     return gemm_blockscaled(A_codes, A_scales, A_tscale, B_codes, B_scales, B_tscale, M, N, K, fmt, out_dt, out,
                             workspace, stream, &ep);
@@ -1232,7 +1232,7 @@ int gemm_epilogue(const uint8_t *A_codes, const uint8_t *A_scales, const float *
 
 size_t gemm_epilogue_workspace(int64_t M, int64_t N, int64_t K, qfp4_fmt fmt)
 {
-    return M <= FW_ROWS ? 0 : gemm_workspace(M, N, K, fmt);
+    return gemm_few_fits(M, N) ? 0 : gemm_workspace(M, N, K, fmt);
 }
 
 // ------------------------------------------------------------------ fused rotate + quantize + GEMM

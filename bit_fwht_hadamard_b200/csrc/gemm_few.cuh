@@ -16,10 +16,10 @@
 
 namespace qfp4 {
 
-constexpr int FW_ROWS = 128;               // most rows of A
+constexpr int FW_ROWS = 128;               // rows of A a CTA
 constexpr int FW_BN = 128;                 // output columns a CTA
 // warps: 0 and 2 producers of B and A, 1 MMA, 3 idle, 4-7 and 8-11 scales of
-// the even and the odd k-tiles; the first eight then finish the sums
+// the even and the odd k-tiles; all twelve then finish the sums
 constexpr int FW_THREADS = 384;
 constexpr int FW_MAX_STAGES = 10;
 constexpr int FW_SF_BUFS = 5;
@@ -31,7 +31,8 @@ struct FewParams {
     const uint8_t *sA, *sB;                // row-major scales: M and N rows of Kg
     const float *tA, *tB;
     int M, N, Kg, KT;
-    int rows;                              // M rounded up to 16
+    int tiles_n;
+    int rows;                              // rows a CTA, rounded up to 16
     int split, stages;
     int aligned;                           // a k-tile's scales of a row are one aligned word group
     void *out;
@@ -97,7 +98,9 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 
     constexpr int CPS = gm_cps(FMT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_ctarank()), n0 = static_cast<int>(blockIdx.x / p.split) * FW_BN;
+    const int rank = static_cast<int>(cluster_ctarank()), tile = static_cast<int>(blockIdx.x / p.split);
+    const int n0 = tile % p.tiles_n * FW_BN, r0 = tile / p.tiles_n * FW_ROWS;   // first column, first row
+    const int live = imin(p.M - r0, FW_ROWS);                 // rows of this CTA
     const int kt0 = static_cast<int>(static_cast<int64_t>(p.KT) * rank / p.split);
     const int nkt = static_cast<int>(static_cast<int64_t>(p.KT) * (rank + 1) / p.split) - kt0;   // at least one
     const int w_bytes = FW_BN * GM_BKB, x_bytes = p.rows * GM_BKB, stage_bytes = w_bytes + x_bytes;
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         // ------------------------------------------------ producers
         if (lane == 0) {
             const CUtensorMap *map = warp == 0 ? &tmW : &tmX;
-            const int bytes = warp == 0 ? w_bytes : x_bytes, row = warp == 0 ? n0 : 0, off = warp == 0 ? 0 : w_bytes;
+            const int bytes = warp == 0 ? w_bytes : x_bytes, row = warp == 0 ? n0 : r0, off = warp == 0 ? 0 : w_bytes;
             int s = 0;
             uint32_t ph = 1;
             for (int i = 0; i < nkt; ++i) {
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         auto load_tile = [&](int i, int u) {                  // k-tile i of this CTA
             load_words(p.sB, p.N, n0 + 32 * q + lane, kt0 + i, rw[u]);
 #pragma unroll
-            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, 32 * m + lane, kt0 + i, rx[u][m]);
+            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, r0 + 32 * m + lane, kt0 + i, rx[u][m]);
         };
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) load_tile(odd + 2 * u, u);
@@ -274,10 +277,11 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         }
     }
     // ---------------------------------------------------- this CTA's sums: all
-    // eight warps, a quadrant of outputs and every other 16 rows each
+    // twelve warps, a quadrant of outputs and every third few rows each
     __syncwarp();
     constexpr int EP = fw_ep(NX);
-    const int q = warp & 3, half = warp >> 2, n = n0 + 32 * q + lane;   // half == 2: no part in it
+    constexpr int SETS = FW_THREADS / 128;
+    const int q = warp & 3, set = warp >> 2, n = n0 + 32 * q + lane;
     const uint32_t acc_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const bool ok = warp_wait(&acc_full, 0) && !abort_flag;
     tc_fence_after();
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     const float bias = ep.bias && n < p.N ? ld_as_float(ep.bias, ep.bias_f32, n) : 0.0f;
     float *sums = reinterpret_cast<float *>(smem);            // [row][128], once every stage has been read (acc_full)
     if (p.split == 1) {
-        for (int m0 = EP * half; m0 < p.M && half < 2; m0 += 2 * EP) {
+        for (int m0 = EP * set; m0 < live; m0 += SETS * EP) {
             uint32_t r[EP];
             if constexpr (EP == 4) tmem_ld4(acc_lane + m0, r);
             else tmem_ld8(acc_lane + m0, r);
@@ -297,11 +301,11 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
             for (int t = 0; t < EP; ++t) v[t] = __uint_as_float(r[t]);
             if (ok && n < p.N)
-                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, p.N, p.M - m0, alpha, step, v, bias);
+                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(r0 + m0) * p.N + n, p.N, live - m0, alpha, step, v, bias);
             __syncwarp();
         }
     } else {
-        for (int m0 = 16 * half; m0 < p.M && half < 2; m0 += 32) {
+        for (int m0 = 16 * set; m0 < live; m0 += 16 * SETS) {
             uint32_t r[16];
             tmem_ld16(acc_lane + m0, r);
             tmem_ld_wait();
@@ -310,12 +314,12 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
             for (int t = 0; t < 16; ++t) sums[(m0 + t) * FW_BN + 32 * q + lane] = __uint_as_float(r[t]);
         }
         cluster_sync();                                       // every CTA's sums are in its shared memory
-        // rows rank, rank + split, ..: EP of them at a time, the two halves in turn
+        // rows rank, rank + split, ..: EP of them at a time, the sets in turn
         const uint32_t base = smem_u32(smem) + 4 * (32 * q + lane);
-        if (ok && n < p.N && half < 2)
+        if (ok && n < p.N)
 #pragma unroll 1
-            for (int m0 = rank + EP * half * p.split; m0 < p.M; m0 += 2 * EP * p.split) {
-                const int nm = imin(EP, (p.M - m0 + p.split - 1) / p.split);
+            for (int m0 = rank + EP * set * p.split; m0 < live; m0 += SETS * EP * p.split) {
+                const int nm = imin(EP, (live - m0 + p.split - 1) / p.split);
                 const uint32_t from = base + 4 * FW_BN * m0;
                 float v[EP];
 #pragma unroll
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
                     for (int r = 1; r < FW_MAX_SPLIT; ++r) v[t] += x[r];
                 }
-                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
+                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(r0 + m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
                                alpha, step, v, bias);
             }
         __syncwarp();
@@ -348,7 +352,7 @@ static int launch_few_nx(const CUtensorMap &tw, const CUtensorMap &tx, const Few
 {
     if (ensure_dyn_smem<k_gemm_few<FMT, OUT, NX>>(FW_SMEM_MAX + 1024) != QFP4_OK) return QFP4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((p.N + FW_BN - 1) / FW_BN * p.split), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles_n * ((p.M + FW_ROWS - 1) / FW_ROWS) * p.split), 1, 1);
     cfg.blockDim = dim3(FW_THREADS, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = s;
@@ -377,6 +381,14 @@ static int launch_few(const CUtensorMap &tw, const CUtensorMap &tx, const FewPar
                         : launch_few_nx<FMT, OUT, 4>(tw, tx, p, ep, smem, s);
 }
 
+static int64_t gemm_few_tiles(int64_t M, int64_t N)
+{
+    return ((N + FW_BN - 1) / FW_BN) * ((M + FW_ROWS - 1) / FW_ROWS);
+}
+
+// Up to 128 rows, and more where one tile an SM takes all of them.
+static bool gemm_few_fits(int64_t M, int64_t N) { return M <= FW_ROWS || gemm_few_tiles(M, N) <= 148; }
+
 static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                     const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
                     const EpParams &ep, qfp4_dtype out_dt, void *out, cudaStream_t stream)
@@ -390,11 +402,12 @@ static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float
     p.N = static_cast<int>(N);
     p.Kg = static_cast<int>(K / (fmt == QFP4_NVFP4 ? 16 : 32));
     p.KT = static_cast<int>((K + gm_bk(fmt) - 1) / gm_bk(fmt));
-    p.rows = static_cast<int>((M + 15) / 16 * 16);
+    p.tiles_n = static_cast<int>((N + FW_BN - 1) / FW_BN);
+    p.rows = static_cast<int>(imin<int64_t>((M + 15) / 16 * 16, FW_ROWS));
     p.aligned = K % gm_bk(fmt) == 0;
     p.out = out;
     // as many CTAs as there are SMs, by splitting K (a CTA keeps two k-tiles at least)
-    const int64_t tiles = (N + FW_BN - 1) / FW_BN;
+    const int64_t tiles = gemm_few_tiles(M, N);
     p.split = static_cast<int>(imax<int64_t>(1, imin<int64_t>(imin<int64_t>(FW_MAX_SPLIT, 148 / tiles), p.KT / 2)));
     // all of a CTA's k-tiles under way at once, where shared memory allows
     const int stage = (FW_BN + p.rows) * GM_BKB;

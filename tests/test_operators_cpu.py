@@ -96,11 +96,15 @@ def test_gemm_epilogue_refusals():
     assert _gemm(out=None) == q.ERR_ARG
     assert _gemm(fmt=q.NVFP4, ts=None) == q.ERR_ARG
     assert _gemm(a=F + 8) == q.ERR_ALIGN
-    M, N, K = 256, 512, 1024
+    M, N, K = 4096, 4096, 1024
     need = q.qfp4_gemm_epilogue_workspace_bytes(M, N, K, 0)
     assert need > 0
     assert _gemm(M=M, N=N, K=K, wsb=need - 1) == q.ERR_ARG
     assert _gemm(M=M, N=N, K=K, ws=None) == q.ERR_ARG
+    # few tiles, and empty calls, need none
+    assert q.qfp4_gemm_epilogue_workspace_bytes(1, 4096, 4096, q.NVFP4) == 0
+    assert q.qfp4_gemm_epilogue_workspace_bytes(128, 14336, 4096, q.MXFP8) == 0
+    assert q.qfp4_gemm_epilogue_workspace_bytes(0, 4096, 4096, q.NVFP4) == 0
 
 
 @pytest.mark.parametrize("bad,status", [
