@@ -124,10 +124,10 @@ static int column_sums(const float *partial, int64_t rows, int64_t N, int TW, in
 // 16-byte accesses; the vectors that straddle a row's ends go element by
 // element.  Reads dY and Z once, writes dZ once: bound by memory.
 constexpr int EB_TILE = 32;                                   // vectors of a block's column tile
-constexpr int EB_U = 1, EB_BLOCKS = 4, EB_WAVE = 4;
+constexpr int EB_BLOCKS = 4, EB_WAVE = 4;
 
 // Grid of the kernel: column tiles, row chunks (each a multiple of eight
-// rows) for EB_WAVE blocks an SM.
+// rows) for at most EB_WAVE blocks an SM, so that all run at once.
 struct EbGrid {
     int tiles, chunks;
     int64_t rows;
@@ -137,82 +137,74 @@ static EbGrid epilogue_backward_grid(int64_t M, int64_t N, int V)
     EbGrid g;
     const int64_t tw = EB_TILE * V;
     g.tiles = static_cast<int>((N % V ? N + V - 1 : N) / tw + ((N % V ? N + V - 1 : N) % tw != 0));
-    const int64_t want = imax<int64_t>(1, imin<int64_t>((EB_WAVE * 148 + g.tiles - 1) / g.tiles, 512));
+    const int64_t want = imax<int64_t>(1, imin<int64_t>(EB_WAVE * 148 / g.tiles, 512));
     g.rows = ((M + want - 1) / want + 7) / 8 * 8;
     g.chunks = static_cast<int>((M + g.rows - 1) / g.rows);
     return g;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256, EB_BLOCKS) k_epilogue_backward(const void *dy, const void *z, int64_t M, int64_t N,
-                                                            int64_t rows, int act, DropParams d, void *dz,
-                                                            float *partial)
+template <int DT, bool SHIFT>
+__global__ void __launch_bounds__(256, EB_BLOCKS) k_epilogue_backward(const void *dy, const void *z, int64_t M,
+                                                                       int64_t N, int64_t rows, int act, DropParams d,
+                                                                       void *dz, float *partial)
 {
-    constexpr int V = DT == QFP4_F32 ? 4 : 8, U = EB_U, TW = EB_TILE * V;
+    constexpr int V = DT == QFP4_F32 ? 4 : 8, TW = EB_TILE * V;
     __shared__ float red[8][TW + V];
     pdl_wait();
     pdl_trigger();
     const uint64_t step = drop_step(d);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int off = static_cast<int>((w * (N & 7)) & (V - 1));
+    const int off = SHIFT ? static_cast<int>((w * (N & 7)) & (V - 1)) : 0;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * TW + lane * V - off;   // this lane's first column
-    const bool full = c0 >= 0 && c0 + V <= N, some = c0 + V > 0 && c0 < N;
+    // without SHIFT a lane's columns are all in the row, or none
+    const bool full = SHIFT ? c0 >= 0 && c0 + V <= N : c0 < N, some = SHIFT ? c0 + V > 0 && c0 < N : full;
     const int64_t m0 = blockIdx.y * rows, m1 = imin(M, m0 + rows);
     const bool use_z = act != QFP4_ACT_NONE;
     Fv<V> sums = Fv<V>::splat(0.0f);
-    // rows m, m + 8, .. of this warp, U at a time; the next ones are loaded
-    // before the present ones are worked on
-    Vec<DT, V> g[U], a[U], gn[U], an[U];
-    auto load = [&](int64_t m, Vec<DT, V> *pg, Vec<DT, V> *pa) {
+    // rows m, m + 8, .. of this warp; the next one is loaded before the
+    // present one is worked on
+    Vec<DT, V> gn, an;
+    auto load = [&](int64_t m) {
+        const int64_t i = m * N + c0;
+        if (full) {
+            gn.load(dy, i);
+            if (use_z) an.load(z, i);
+        } else if constexpr (SHIFT) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = (m + 8 * u) * N + c0;
-            if (m + 8 * u < m1 && full) {
-                pg[u].load(dy, i);
-                if (use_z) pa[u].load(z, i);
-            } else {
+            for (int k = 0; k < 4; ++k) gn.r[k] = an.r[k] = 0u;
+            if (some) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pg[u].r[k] = pa[u].r[k] = 0u;
-                if (m + 8 * u < m1 && some) {
-#pragma unroll
-                    for (int t = 0; t < V; ++t)
-                        if (c0 + t >= 0 && c0 + t < N) {
-                            pg[u].load1(dy, i, t);
-                            if (use_z) pa[u].load1(z, i, t);
-                        }
-                }
+                for (int t = 0; t < V; ++t)
+                    if (c0 + t >= 0 && c0 + t < N) {
+                        gn.load1(dy, i, t);
+                        if (use_z) an.load1(z, i, t);
+                    }
             }
         }
     };
-    load(m0 + w, gn, an);
-    for (int64_t m = m0 + w; m < m1; m += 8 * U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            g[u] = gn[u];
-            a[u] = an[u];
-        }
-        load(m + 8 * U, gn, an);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (m + 8 * u >= m1 || !some) continue;
-            const int64_t i = (m + 8 * u) * N + c0;             // a multiple of V
+    if (some && m0 + w < m1) load(m0 + w);
+    if (some)
+        for (int64_t m = m0 + w; m < m1; m += 8) {
+            Vec<DT, V> g = gn;
+            const Vec<DT, V> a = an;
+            if (m + 8 < m1) load(m + 8);
+            const int64_t i = m * N + c0;                       // a multiple of V
             float v[V], x[V];
-            g[u].get(v);
+            g.get(v);
             if (d.on) drop_values<V, true>(d, step, i, v);
             if (use_z) {
-                a[u].get(x);
+                a.get(x);
                 act_backward<V>(v, x, act);
             }
             sums = sums + Fv<V>::of(v);                         // zero outside the row
-            g[u].set(v);
-            if (full) g[u].store(dz, i);
-            else {
+            g.set(v);
+            if (full) g.store(dz, i);
+            else if constexpr (SHIFT) {
 #pragma unroll
                 for (int t = 0; t < V; ++t)
-                    if (c0 + t >= 0 && c0 + t < N) g[u].store1(dz, i, t);
+                    if (c0 + t >= 0 && c0 + t < N) g.store1(dz, i, t);
             }
         }
-    }
     if (!partial) return;
     // slot V + j of red: column blockIdx.x TW + j; a warp covers j = -off .. TW - off - 1
     for (int j = lane; j < V; j += 32) red[w][j] = red[w][TW + j] = 0.0f;
@@ -237,8 +229,13 @@ static int epilogue_backward(const void *dY, const void *Z, int64_t M, int64_t N
 {
     constexpr int V = DT == QFP4_F32 ? 4 : 8;
     const EbGrid g = epilogue_backward_grid(M, N, V);
-    if (launch_pdl(k_epilogue_backward<DT>, dim3(g.tiles, g.chunks), dim3(256), 0, s, dY, Z, M, N, g.rows, act, d, dZ,
-                   dbias ? partial : nullptr) != cudaSuccess) {
+    float *sums = dbias ? partial : nullptr;
+    const dim3 grid(g.tiles, g.chunks);
+    const cudaError_t e = N % V ? launch_pdl(k_epilogue_backward<DT, true>, grid, dim3(256), 0, s, dY, Z, M, N, g.rows,
+                                             act, d, dZ, sums)
+                                : launch_pdl(k_epilogue_backward<DT, false>, grid, dim3(256), 0, s, dY, Z, M, N, g.rows,
+                                             act, d, dZ, sums);
+    if (e != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
