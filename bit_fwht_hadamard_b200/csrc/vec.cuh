@@ -23,13 +23,17 @@ struct Fv {
     {
         Fv o;
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) o.p[k] = f2pack(v[2 * k], v[2 * k + 1]);
+        for (int k = 0; k < V / 2; ++k)
+            o.p[k] = static_cast<uint64_t>(__float_as_uint(v[2 * k + 1])) << 32 | __float_as_uint(v[2 * k]);
         return o;
     }
     __device__ __forceinline__ void to(float *v) const
     {
 #pragma unroll
-        for (int k = 0; k < V / 2; ++k) f2unpack(p[k], v[2 * k], v[2 * k + 1]);
+        for (int k = 0; k < V / 2; ++k) {
+            v[2 * k] = __uint_as_float(static_cast<uint32_t>(p[k]));
+            v[2 * k + 1] = __uint_as_float(static_cast<uint32_t>(p[k] >> 32));
+        }
     }
     __device__ __forceinline__ float sum() const
     {
