@@ -21,7 +21,9 @@
 // tile's MMAs overlap the stores.  The row-major scales are first rearranged
 // by a small prepass into 512-byte chunks (128 rows x 4 scales: byte
 // (r%32)*16 + (r/32)*4 + j), which the main loops load with plain TMA or
-// bulk copies; the chunks live in the caller's workspace.
+// bulk copies; the chunks live in the caller's workspace.  A product with an
+// epilogue (bias, activation, dropout, residual) runs on k_gemm_bs2 as well, or
+// on k_gemm_few (gemm_few.cuh) where the output is small.
 #include <type_traits>
 
 #include "qfp4_common.cuh"
@@ -282,15 +284,13 @@ __global__ void __launch_bounds__(256) k_sf_chunks(SfJob ja, SfJob jb, int Kg, i
 }
 
 // ------------------------------------------------------------------ main kernel
-template <int FMT, int OUT, bool EP>
+template <int FMT, int OUT>
 __global__ void __launch_bounds__(GM_THREADS, 1)
-    k_gemm_blockscaled(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p,
-                       EpParams ep)
+    k_gemm_blockscaled(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[GM_STAGES], empty[GM_STAGES], acc_full, acc_empty, drain;
-    __shared__ float4 bias_sh[EP ? 2 : 1][EP ? 64 : 1];   // by tile parity
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int abort_flag;
 
@@ -410,31 +410,17 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         const int h = (warp - 2) >> 2;            // column half
         float alpha = 1.0f;
         if (FMT == QFP4_NVFP4) alpha = __fmul_rn(*p.tA, *p.tB);
-        const uint64_t step = EP ? drop_step(ep.drop) : 0ull;
         int ti = 0;
         for (int t = blockIdx.x; t < ntiles && !abort_flag; t += gridDim.x, ++ti) {
             int mb, nb;
             tile_coords(t, p.tiles_m, p.tiles_n, mb, nb);
-            float4 bias4 = {};
-            if constexpr (EP) bias4 = bias4_load(ep, nb * GM_BN + 128 * h + 4 * lane, p.N - nb * GM_BN - 128 * h - 4 * lane);
             if (!warp_wait(&acc_full, ti & 1)) { abort_flag = 1; break; }
             tc_fence_after();
-            if constexpr (EP) {
-                bias_sh[ti & 1][32 * h + lane] = bias4;
-                __syncwarp();
-            }
+            // two 16-lane halves of this warp's quadrant, 128 columns each
             uint32_t r[128];
-            if constexpr (EP) {
-                // a lane a row: 128 columns of its own
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32(tmem + (static_cast<uint32_t>(32 * q) << 16) + 128 * h + 32 * c, r + 32 * c);
-            } else {
-                // two 16-lane halves of this warp's quadrant, 128 columns each
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                    tmem_ld16x256b_x16(tmem + (static_cast<uint32_t>(32 * q + 16 * hh) << 16) + 128 * h, r + 64 * hh);
-            }
+            for (int hh = 0; hh < 2; ++hh)
+                tmem_ld16x256b_x16(tmem + (static_cast<uint32_t>(32 * q + 16 * hh) << 16) + 128 * h, r + 64 * hh);
             tmem_ld_wait();
             reg_fence<128>(r);
             // the accumulator is in registers: hand it back before the stores
@@ -442,12 +428,6 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty);
 
-            if constexpr (EP) {
-                const int row = mb * GM_BM + 32 * q + lane;
-                if (row < p.M)
-                    ep_row128<OUT>(ep, p.out, p.N, row, nb * GM_BN + 128 * h, alpha, step, r, bias_sh[ti & 1] + 32 * h);
-                continue;
-            }
             // r[64hh + 4j + {0,1}]: row 32q + 16hh + lane/4, columns 8j + 2(lane%4) + {0,1};
             // r[64hh + 4j + {2,3}]: the row 8 below.  Four lanes cover 32 contiguous bytes.
             const int col0 = nb * GM_BN + 128 * h + 2 * (lane & 3);
@@ -1030,13 +1010,12 @@ int rearrange_scales(const uint8_t *a_scales, int64_t M, int n_blocks_a, uint8_t
     return QFP4_OK;
 }
 
-template <int FMT, int OUT, bool EP>
-static int launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const GemmParams &p, const EpParams &ep, int grid,
-                       cudaStream_t s)
+template <int FMT, int OUT>
+static int launch_gemm(const CUtensorMap &ta, const CUtensorMap &tb, const GemmParams &p, int grid, cudaStream_t s)
 {
-    auto kern = k_gemm_blockscaled<FMT, OUT, EP>;
-    if (ensure_dyn_smem<k_gemm_blockscaled<FMT, OUT, EP>>(GM_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
-    if (launch_pdl(kern, dim3(grid), dim3(GM_THREADS), GM_SMEM, s, ta, tb, p, ep) != cudaSuccess) {
+    auto kern = k_gemm_blockscaled<FMT, OUT>;
+    if (ensure_dyn_smem<k_gemm_blockscaled<FMT, OUT>>(GM_SMEM) != QFP4_OK) return QFP4_ERR_CUDA;
+    if (launch_pdl(kern, dim3(grid), dim3(GM_THREADS), GM_SMEM, s, ta, tb, p) != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
@@ -1092,8 +1071,9 @@ static int dispatch_gemm(qfp4_fmt fmt, qfp4_dtype out_dt, const EpParams *epi, F
 
 // Main kernel on already rearranged scales (sfa / sfb in the chunk layout).
 // Problems taller than one 128-row block run on CTA pairs (256 x 256 tiles),
-// the rest on single CTAs (128 x 256 tiles).  epi: the epilogue's options,
-// or NULL for the plain product.
+// the rest on single CTAs (128 x 256 tiles).  epi: the epilogue's options, or
+// NULL for the plain product; only CTA pairs have one (gemm_epilogue() gives
+// 128 rows and fewer to k_gemm_few).
 int gemm_core(const uint8_t *A_codes, const uint8_t *sfa, const float *A_tscale, const uint8_t *B_codes,
               const uint8_t *sfb, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
               qfp4_dtype out_dt, void *out, cudaStream_t stream,
@@ -1160,9 +1140,8 @@ int gemm_core(const uint8_t *A_codes, const uint8_t *sfa, const float *A_tscale,
         });
     }
     const int grid = static_cast<int>(imin<int64_t>(static_cast<int64_t>(L.MB) * L.NT, num_sms()));
-    return dispatch_gemm(fmt, out_dt, epi, [&](auto f, auto o, auto e) {
-        return launch_gemm<f.value, o.value, e.value>(ta, tb, p, epi ? *epi : EpParams{}, grid, stream);
-    });
+    return dispatch_gemm(fmt, out_dt, nullptr,
+                         [&](auto f, auto o, auto) { return launch_gemm<f.value, o.value>(ta, tb, p, grid, stream); });
 }
 
 int gemm_blockscaled(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
