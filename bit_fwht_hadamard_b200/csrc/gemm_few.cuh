@@ -26,6 +26,12 @@ constexpr int FW_SF_BUFS = 5;
 __host__ __device__ constexpr int fw_ahead(int nx) { return nx == 1 ? 4 : 2; }   // k-tiles of scales in registers a warp
 constexpr int FW_MAX_SPLIT = 8;
 constexpr int FW_SMEM_MAX = 208 * 1024;
+// At least this much, so that an SM never holds two CTAs of these kernels.  Each
+// takes all of tensor memory and waits for its cluster at the end: two clusters
+// of different streams on the same two SMs, each with one CTA that has tensor
+// memory and one that waits for it, would never finish.
+constexpr int FW_SMEM_MIN = 116 * 1024;
+static_assert(2 * FW_SMEM_MIN > 228 * 1024, "one CTA an SM");
 
 struct FewParams {
     const uint8_t *sA, *sB;                // row-major scales: M and N rows of Kg
@@ -413,7 +419,7 @@ static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float
     const int stage = (FW_BN + p.rows) * GM_BKB;
     const int per = (p.KT + p.split - 1) / p.split;
     p.stages = imax(2, imin(imin(FW_MAX_STAGES, per), FW_SMEM_MAX / stage));
-    const int smem = imax(p.stages * stage, p.split > 1 ? p.rows * FW_BN * 4 : 0) + 1024;
+    const int smem = imax(imax(p.stages * stage, p.split > 1 ? p.rows * FW_BN * 4 : 0), FW_SMEM_MIN) + 1024;
     CUtensorMap tw, tx;
     const uint64_t row_bytes = static_cast<uint64_t>(fmt == QFP4_MXFP8 ? K : K / 2);
     {

@@ -499,6 +499,29 @@ def test_operators_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
+@pytest.mark.parametrize("fmt,M,N,K", [("nvfp4", 4, 8960, 1024), ("mxfp8", 20, 4480, 1024), ("mxfp4", 2, 2304, 2048)])
+def test_gemm_epilogue_of_few_rows_on_two_streams_at_once(fmt, M, N, K):
+    """Clusters of two calls that run together: with so short a K two CTAs
+    would fit on an SM, and each takes the whole tensor memory."""
+    calls = []
+    for seed in (1, 11):
+        A, B = R.random_operand(M, K, FMT[fmt], seed), R.random_operand(N, K, FMT[fmt], seed + 1)
+        bias = normal((N,), seed + 2)
+        calls.append(lambda A=A, B=B, bias=bias, **kw: q.gemm_epilogue(A, B, M, N, K, FMT[fmt], bias=bias,
+                                                                       act=q.ACT_SILU, **kw)[0])
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(40):
+        for k in (0, 1):
+            got[k].append(calls[k](stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert all(torch.equal(g, want[k]) for g in got[k])
+    assert q.qfp4_last_device_error() == 0
+
+
 def test_graph_replays_draw_new_masks():
     """The step counter is read when the kernel runs: each replay has its own mask."""
     x = torch.ones((64, 256), device="cuda")
