@@ -615,11 +615,12 @@ _layernorm_backward_ws = functools.lru_cache(1024)(qfp4_layernorm_backward_works
 def _scratch(workspace, nbytes, like, stream):
     """(address, bytes, the tensor that has to live until the call) of the
     caller's workspace, or of a fresh one."""
-    if workspace is None:
-        if not nbytes:
-            return None, 0, None
-        workspace = _new(like, stream, _torch().uint8, nbytes)
-    return workspace.data_ptr(), workspace.nbytes, workspace
+    if workspace is not None:
+        return _tensor(workspace, "workspace", like.get_device()), workspace.nbytes, workspace
+    if not nbytes:
+        return None, 0, None
+    workspace = _new(like, stream, _torch().uint8, nbytes)
+    return workspace.data_ptr(), nbytes, workspace
 
 
 def _operand(q, name, rows, K, fmt, index):

@@ -592,6 +592,13 @@ def test_refusals_of_the_wrappers_on_cuda_tensors():
         q.gemm_epilogue(A, B, 8, 16, 64, q.NVFP4, step=torch.zeros(1, device="cuda"))
     with pytest.raises(q.QFP4Error):
         q.gemm_epilogue(A, B, 8, 16, 64, q.NVFP4, dropout_p=1.0)
+    with pytest.raises(ValueError, match="workspace"):
+        q.epilogue_backward(x, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace"):
+        q.layernorm_backward(x, x, w, x[:, 0].contiguous(), x[:, 1].contiguous(),
+                             workspace=torch.empty((4, 4096), device="cuda").T)
+    with pytest.raises(q.QFP4Error):                          # too small
+        q.epilogue_backward(x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="contiguous"):
         q.dropout(x.T, 0.1)
     with pytest.raises(TypeError):
