@@ -322,9 +322,15 @@ def qfp4_launch_count():
 
 
 # ------------------------------------------------------------------ torch conveniences
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -527,14 +533,14 @@ def linear_backward(G, X, W, fmt=NVFP4, seed=0, out_dtype=None, want_dx=True, wa
 # These wrappers check every tensor they hand over; a call on a few rows costs
 # about as much in Python as on the device, so the checks are one expression
 # where they pass and name the fault only where they fail.
-_current_device = None      # torch.cuda.current_device
+_current_device = None      # the current device's index
 _raw_stream = None          # device index -> handle of its current stream
 
 
 def _cuda_api():
     global _current_device, _raw_stream
     torch = _torch()
-    _current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _tensor(t, name, index, shape=None, dtype=None):
@@ -717,17 +723,19 @@ def epilogue_backward(dY, Z=None, act=ACT_NONE, dropout_p=0.0, seed=0, step=None
     M, N = shape
     dt = _xdt(dY)
     pz = None if Z is None else _tensor(Z, "Z", index, shape, dtype)
-    dZ = db = pb = ws = keep = None
+    dZ = db = pd = pb = ws = keep = None
     wsb = 0
     if out is not None:
         dZ, db = out.get("dZ"), out.get("dbias")
+        pd = None if dZ is None else _tensor(dZ, "dZ", index, shape, dtype)
+        pb = None if db is None else _tensor(db, "dbias", index, (N,), _torch().float32)
     if dZ is None:
         dZ = _new_like(dY, stream)
-    pd = _tensor(dZ, "dZ", index, shape, dtype)
+        pd = dZ.data_ptr()
     if db is None and want_dbias:
         db = _new(dY, stream, _torch().float32, N)
+        pb = db.data_ptr()
     if db is not None:
-        pb = _tensor(db, "dbias", index, (N,), _torch().float32)
         ws, wsb, keep = _scratch(workspace, _epilogue_backward_ws(M, N), dY, stream)
     _call(qfp4_epilogue_backward, index, stream, dY.data_ptr(), pz, dt, M, N, act, dropout_p, seed,
           _step(step, index), pd, pb, ws, wsb)
@@ -775,7 +783,8 @@ def layernorm_forward(x, gamma=None, beta=None, eps=1e-5, want_stats=True, out=N
         y = _new_like(x, stream)
         py, mean, rstd, pm, pr = y.data_ptr(), None, None, None, None
         if want_stats:
-            mean, rstd = _new(x, stream, f32, M), _new(x, stream, f32, M)
+            mean = _new(x, stream, f32, M)
+            rstd = _new_like(mean, stream)
             pm, pr = mean.data_ptr(), rstd.data_ptr()
     else:
         y, mean, rstd = out.get("y"), out.get("mean"), out.get("rstd")
@@ -804,19 +813,22 @@ def layernorm_backward(dy, x, gamma, mean, rstd, want_dx=True, want_dw=True, out
     pg, _, wdt = _norm_params(index, D, gamma, None)
     py = _tensor(dy, "dy", index, shape, dtype)
     pm, pr = _tensor(mean, "mean", index, (M,), f32), _tensor(rstd, "rstd", index, (M,), f32)
-    dx = dg = db = ws = keep = None
+    dx = dg = db = px = pdg = pdb = ws = keep = None
     wsb = 0
     if out is not None:
         dx, dg, db = out.get("dx"), out.get("dgamma"), out.get("dbeta")
+        px = None if dx is None else _tensor(dx, "dx", index, shape, dtype)
+        pdg = None if dg is None else _tensor(dg, "dgamma", index, (D,), f32)
+        pdb = None if db is None else _tensor(db, "dbeta", index, (D,), f32)
     if dx is None and want_dx:
         dx = _new_like(x, stream)
+        px = dx.data_ptr()
     if dg is None and want_dw:
         dg = _new(x, stream, f32, D)
+        pdg = dg.data_ptr()
     if db is None and want_dw:
-        db = _new(x, stream, f32, D)
-    px = None if dx is None else _tensor(dx, "dx", index, shape, dtype)
-    pdg = None if dg is None else _tensor(dg, "dgamma", index, (D,), f32)
-    pdb = None if db is None else _tensor(db, "dbeta", index, (D,), f32)
+        db = _new_like(dg, stream)
+        pdb = db.data_ptr()
     if dg is not None or db is not None:
         ws, wsb, keep = _scratch(workspace, _layernorm_backward_ws(M, D), x, stream)
     _call(qfp4_layernorm_backward, index, stream, py, x.data_ptr(), dt, M, D, pg, wdt, pm, pr, px, pdg, pdb, ws, wsb)
