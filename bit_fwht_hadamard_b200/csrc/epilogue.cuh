@@ -351,6 +351,12 @@ __device__ __forceinline__ float4 bias4_load(const EpParams &ep, int col, int nc
     return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
 }
 
+// A lane has a row and works on sixteen columns at a time, whole 32-byte
+// sectors: 8192 x 11008 x 4096 NVFP4 with bias, GELU and z kept took 693 us on
+// the plain product's fragments (two columns a lane, one element at a time),
+// 322 a lane a row, 220 with GELU's polynomial and the bias staged (256 in a
+// sustained loop, under the power cap; the product alone 194).
+//
 // The last step of qfp4_gemm_epilogue on the accumulators acc[0 .. 15] of one
 // row's columns col .. col + 15 (the first nc of them exist; nc and col are
 // multiples of 4), i = row * N + col: z = alpha acc + bias, the optional copy

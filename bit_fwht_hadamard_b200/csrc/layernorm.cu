@@ -418,7 +418,9 @@ __global__ void __launch_bounds__(GR *G)
 // (256, 8192]): the same pass with the rows of dy and x brought into shared
 // memory by bulk copies, `stages` rows ahead, so that no register waits for
 // memory, and gamma beside them (in L1 it gave way to dx: 8192 x 4096 bf16 52 us
-// against 50, binary32 79 against 72).  One block an SM of GR groups of G threads, each group with rows, a
+// against 49, 31 from memory alone; binary32 79 against 71).  Bound by the latency
+// of a row: shared memory, two sums over the group, 24 instructions an element
+// (fetching the next row's values before those sums: 51 us).  One block an SM of GR groups of G threads, each group with rows, a
 // ring and a named barrier of its own; a thread holds NV vectors' columns.
 // The groups' sums are joined at the end, so there are no more partial rows
 // than SMs.  KEEP: xhat and g stay in registers between the row sums and dx;
