@@ -11,8 +11,8 @@
 // The CTAs of a cluster add their sums through distributed shared memory, in
 // the order of their k ranges; each then finishes some of the rows.
 //
-// On the device, bias and SiLU: 1 x 4096 x 4096 MXFP8 8.7 us (2.6 from memory
-// alone), 8 x 11008 x 4096 MXFP4 9.3, 100 x 11008 x 4096 MXFP4 12.7 (4.0 from
+// On the device, bias and SiLU: 1 x 4096 x 4096 MXFP8 8.0 us (2.6 from memory
+// alone), 8 x 11008 x 4096 MXFP4 8.5, 100 x 11008 x 4096 MXFP4 11.5 (4.0 from
 // memory alone; its 86 tiles run on 86 SMs, and halves of K would need 172).
 // What is left is the launch and a CTA's chain of barriers.
 #pragma once
@@ -37,6 +37,7 @@ constexpr int FW_SMEM_MAX = 208 * 1024;
 // memory and one that waits for it, would never finish.
 constexpr int FW_SMEM_MIN = 116 * 1024;
 static_assert(2 * FW_SMEM_MIN > 228 * 1024, "one CTA an SM");
+static_assert(FW_ROWS * FW_BN * 4 <= FW_SMEM_MIN, "the sums");
 
 struct FewParams {
     const uint8_t *sA, *sB;                // row-major scales: M and N rows of Kg
@@ -49,47 +50,92 @@ struct FewParams {
     void *out;
 };
 
-__device__ __forceinline__ float ld_dsmem(uint32_t cluster_addr)
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t cluster_addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
     return v;
 }
 
-// The epilogue of one column of the output, n (this thread's): element i0 + t
-// `stride` elements is row t of the nm rows (at most EP) that exist.  Few
-// rows at a time, so that the code stays short: with a row or two to finish,
-// fetching it is what the epilogue costs (sixteen at a time took 3 us more).
-__host__ __device__ constexpr int fw_ep(int nx) { return nx == 1 ? 4 : 8; }
+// The epilogue of U quads of columns: quad u is elements i0 + u stride ..
+// i0 + u stride + 3 (multiples of 4), the first nu of them exist.  Few quads at
+// a time, so that the code stays short: with a row or two to finish, fetching
+// it is what the epilogue costs.
+__host__ __device__ constexpr int fw_quads(int nx) { return nx == 1 ? 1 : 2; }
+template <int OUT, int U>
+__device__ __forceinline__ void ep_quads(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nu, float alpha,
+                                         uint64_t step, const float4 *acc, float4 bias)
+{
+    float res[4 * U], v[4 * U];
+    if (ep.residual)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < nu) {
+                const int64_t i = i0 + u * stride;
+                if (ep.residual_f32)
+                    *reinterpret_cast<float4 *>(res + 4 * u) =
+                        *reinterpret_cast<const float4 *>(static_cast<const float *>(ep.residual) + i);
+                else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(ep.residual) + i);
+                    *reinterpret_cast<float4 *>(res + 4 * u) = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+                }
+            }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        v[4 * u] = fmaf(acc[u].x, alpha, bias.x);
+        v[4 * u + 1] = fmaf(acc[u].y, alpha, bias.y);
+        v[4 * u + 2] = fmaf(acc[u].z, alpha, bias.z);
+        v[4 * u + 3] = fmaf(acc[u].w, alpha, bias.w);
+    }
+    auto store = [&](void *p) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < nu) {
+                const int64_t i = i0 + u * stride;
+                if (OUT == QFP4_F32)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) =
+                        make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
+                        make_uint2(pack_bf16(v[4 * u], v[4 * u + 1]), pack_bf16(v[4 * u + 2], v[4 * u + 3]));
+            }
+    };
+    if (ep.preact) store(ep.preact);
+    act_forward<4 * U>(v, ep.act);
+    if (ep.drop.on)
+#pragma unroll
+        for (int u = 0; u < U; ++u) drop_values<4, true>(ep.drop, step, i0 + u * stride, v + 4 * u);
+    if (ep.residual)
+#pragma unroll
+        for (int t = 0; t < 4 * U; ++t) v[t] += res[t];
+    store(out);
+}
+
+// The epilogue without dropout of one column of the output: element i0 + t N
+// is row t of the nm rows (at most EP) that exist.
 template <int OUT, int EP>
-__device__ __forceinline__ void ep_column(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nm,
-                                          float alpha, uint64_t step, const float *acc, float bias)
+__device__ __forceinline__ void ep_column(const EpParams &ep, void *out, int64_t i0, int64_t N, int nm, float alpha,
+                                          const uint32_t *acc, float bias)
 {
     float res[EP], v[EP];
     if (ep.residual)
 #pragma unroll
-        for (int t = 0; t < EP; ++t)
-            res[t] = t < nm ? ld_as_float(ep.residual, ep.residual_f32, i0 + t * stride) : 0.0f;
+        for (int t = 0; t < EP; ++t) res[t] = t < nm ? ld_as_float(ep.residual, ep.residual_f32, i0 + t * N) : 0.0f;
 #pragma unroll
-    for (int t = 0; t < EP; ++t) v[t] = fmaf(acc[t], alpha, bias);
+    for (int t = 0; t < EP; ++t) v[t] = fmaf(__uint_as_float(acc[t]), alpha, bias);
     auto store = [&](void *p) {
 #pragma unroll
         for (int t = 0; t < EP; ++t)
             if (t < nm) {
-                if (OUT == QFP4_F32) static_cast<float *>(p)[i0 + t * stride] = v[t];
-                else static_cast<__nv_bfloat16 *>(p)[i0 + t * stride] = __float2bfloat16_rn(v[t]);
+                if (OUT == QFP4_F32) static_cast<float *>(p)[i0 + t * N] = v[t];
+                else static_cast<__nv_bfloat16 *>(p)[i0 + t * N] = __float2bfloat16_rn(v[t]);
             }
     };
     if (ep.preact) store(ep.preact);
     act_forward<EP>(v, ep.act);
-    if (ep.drop.on) {
-#pragma unroll
-        for (int t = 0; t < EP; ++t) {
-            const uint64_t i = static_cast<uint64_t>(i0 + t * stride), q = i >> 2;
-            const uint4 w = drop_words4(ep.drop, step, static_cast<uint32_t>(q), static_cast<uint32_t>(q >> 32));
-            v[t] = drop1(ep.drop, v[t], i & 2 ? (i & 1 ? w.w : w.z) : (i & 1 ? w.y : w.x));
-        }
-    }
     if (ep.residual)
 #pragma unroll
         for (int t = 0; t < EP; ++t) v[t] += res[t];
@@ -97,7 +143,11 @@ __device__ __forceinline__ void ep_column(const EpParams &ep, void *out, int64_t
 }
 
 // NX: 32-row groups of A whose scales are loaded (1 for up to 32 rows, else 4).
-template <int FMT, int OUT, int NX>
+// PLAIN: wide outputs without a split of K or dropout, scale rows of whole
+// aligned words.  Such calls have kernels of their own because a block lives a
+// few microseconds, of which fetching its code is a part: with both epilogues and
+// both ways of loading scales in one kernel every call took 0.5 to 0.8 us more.
+template <int FMT, int OUT, int NX, bool PLAIN>
 __global__ void __launch_bounds__(FW_THREADS, 1)
     k_gemm_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, FewParams p, EpParams ep)
 {
@@ -196,12 +246,12 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         constexpr int AHEAD = fw_ahead(NX);
         const int q = warp & 3, odd = warp >= 8 ? 1 : 0;
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-        auto load_words = [&](const uint8_t *sc, int R, int row, int kt, uint32_t *w) {
+        auto load_words = [&](const uint8_t *sc, int R, int row, int kt, uint32_t tail, uint32_t *w) {
 #pragma unroll
             for (int c = 0; c < CPS; ++c) w[c] = 0u;
             if (row >= R || kt >= kt0 + nkt) return;
             const uint8_t *s = sc + static_cast<int64_t>(row) * p.Kg + 4 * CPS * kt;
-            if (p.aligned) {
+            if (PLAIN || p.aligned) {
                 if constexpr (CPS == 4) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(s);
                     w[0] = u.x;
@@ -214,10 +264,33 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
                     w[1] = u.y;
                 } else
                     w[0] = *reinterpret_cast<const uint32_t *>(s);
-            } else
-                for (int i = 0; i < 4 * CPS; ++i)
-                    if (4 * CPS * kt + i < p.Kg) w[i >> 2] |= static_cast<uint32_t>(s[i]) << (8 * (i & 3));
+            } else {
+                // the aligned words around the row's bytes [s, last), shifted
+                const int nb = imin(4 * CPS, p.Kg - 4 * CPS * kt), sh = 8 * static_cast<int>(reinterpret_cast<uintptr_t>(s) & 3);
+                const uint8_t *last = s + nb, *end = sc + static_cast<int64_t>(R) * p.Kg, *a = s - sh / 8;
+                auto word = [&](const uint8_t *at) -> uint32_t {
+                    return at >= last ? 0u : at + 4 <= end ? *reinterpret_cast<const uint32_t *>(at) : tail;
+                };
+                uint32_t lo = word(a);
+#pragma unroll
+                for (int c = 0; c < CPS; ++c) {
+                    const uint32_t hi = word(a + 4 * c + 4), v = __funnelshift_r(lo, hi, sh);
+                    const int n = nb - 4 * c;                 // of this word's bytes, the row's
+                    w[c] = n >= 4 ? v : n <= 0 ? 0u : v & ((1u << (8 * n)) - 1u);
+                    lo = hi;
+                }
+            }
         };
+        // the last, partial word of a scale array of that many bytes
+        auto tail_word = [&](const uint8_t *sc, int64_t bytes) {
+            uint32_t v = 0u;
+            if (!PLAIN && !p.aligned)
+                for (int i = 0; i < static_cast<int>(bytes & 3); ++i)
+                    v |= static_cast<uint32_t>(sc[(bytes & ~int64_t(3)) + i]) << (8 * i);
+            return v;
+        };
+        const uint32_t tail_b = tail_word(p.sB, static_cast<int64_t>(p.N) * p.Kg);
+        const uint32_t tail_a = tail_word(p.sA, static_cast<int64_t>(p.M) * p.Kg);
         // the scale bytes of this thread's row of B, all of them, into L2: the
         // loads below reach only a few k-tiles, less than memory's latency
         if (n0 + 32 * q + lane < p.N && !odd) {
@@ -227,9 +300,9 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
         }
         uint32_t rw[AHEAD][CPS], rx[AHEAD][NX][CPS];
         auto load_tile = [&](int i, int u) {                  // k-tile i of this CTA
-            load_words(p.sB, p.N, n0 + 32 * q + lane, kt0 + i, rw[u]);
+            load_words(p.sB, p.N, n0 + 32 * q + lane, kt0 + i, tail_b, rw[u]);
 #pragma unroll
-            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, r0 + 32 * m + lane, kt0 + i, rx[u][m]);
+            for (int m = 0; m < NX; ++m) load_words(p.sA, p.M, r0 + 32 * m + lane, kt0 + i, tail_a, rx[u][m]);
         };
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) load_tile(odd + 2 * u, u);
@@ -287,35 +360,45 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
             }
         }
     }
-    // ---------------------------------------------------- this CTA's sums: all
-    // twelve warps, a quadrant of outputs and every third few rows each
+    // ---------------------------------------------------- this CTA's sums, by
+    // all twelve warps.  PLAIN: a thread a column, straight from tensor memory
+    // (100 x 11008 x 4096 11.5 us on the device, the other way 13.6).  Else
+    // through shared memory as [row][128], then quads of columns of this CTA's
+    // rows over all threads: one generator call a quad, and no idle threads where
+    // the output is narrow (100 x 11008 x 4096 with dropout 17.0 us, a thread a
+    // column 20.5; 12440 x 32 x 704 9.6 and 18).
     __syncwarp();
-    constexpr int EP = fw_ep(NX);
+    constexpr int U = fw_quads(NX);
     constexpr int SETS = FW_THREADS / 128;
-    const int q = warp & 3, set = warp >> 2, n = n0 + 32 * q + lane;
+    const int q = warp & 3, set = warp >> 2;
     const uint32_t acc_lane = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const int quads = imin(FW_BN, p.N - n0) / 4, qd = static_cast<int>(threadIdx.x) % quads;
+    const int n = n0 + 32 * q + lane;                         // PLAIN: this thread's column
+    float4 bias = {};                                         // on its way while the sums are finished
+    if (!PLAIN) bias = bias4_load(ep, n0 + 4 * qd, 4);
+    else if (ep.bias && n < p.N) bias.x = ld_as_float(ep.bias, ep.bias_f32, n);
     const bool ok = warp_wait(&acc_full, 0) && !abort_flag;
     tc_fence_after();
     float alpha = 1.0f;
     if (FMT == QFP4_NVFP4) alpha = __fmul_rn(*p.tA, *p.tB);
-    const uint64_t step = drop_step(ep.drop);
-    const float bias = ep.bias && n < p.N ? ld_as_float(ep.bias, ep.bias_f32, n) : 0.0f;
-    float *sums = reinterpret_cast<float *>(smem);            // [row][128], once every stage has been read (acc_full)
-    if (p.split == 1) {
+    const uint64_t step = PLAIN ? 0ull : drop_step(ep.drop);
+    float *sums = reinterpret_cast<float *>(smem);            // once every stage has been read (acc_full)
+    if constexpr (PLAIN) {
+        constexpr int EP = 4 * U;
         for (int m0 = EP * set; m0 < live; m0 += SETS * EP) {
             uint32_t r[EP];
             if constexpr (EP == 4) tmem_ld4(acc_lane + m0, r);
             else tmem_ld8(acc_lane + m0, r);
             tmem_ld_wait();
             reg_fence<EP>(r);
-            float v[EP];
-#pragma unroll
-            for (int t = 0; t < EP; ++t) v[t] = __uint_as_float(r[t]);
             if (ok && n < p.N)
-                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(r0 + m0) * p.N + n, p.N, live - m0, alpha, step, v, bias);
+                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(r0 + m0) * p.N + n, p.N, live - m0, alpha, r, bias.x);
             __syncwarp();
         }
     } else {
+        // (a CTA's rows, `rows` at a time: rank, rank + split, .., `count` of them)
+        const int rows = FW_THREADS / quads, first = static_cast<int>(threadIdx.x) / quads;
+        const int count = (live - rank + p.split - 1) / p.split;
         for (int m0 = 16 * set; m0 < live; m0 += 16 * SETS) {
             uint32_t r[16];
             tmem_ld16(acc_lane + m0, r);
@@ -324,32 +407,43 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
 #pragma unroll
             for (int t = 0; t < 16; ++t) sums[(m0 + t) * FW_BN + 32 * q + lane] = __uint_as_float(r[t]);
         }
-        cluster_sync();                                       // every CTA's sums are in its shared memory
-        // rows rank, rank + split, ..: EP of them at a time, the sets in turn
-        const uint32_t base = smem_u32(smem) + 4 * (32 * q + lane);
-        if (ok && n < p.N)
+        // every CTA's sums are in its shared memory
+        if (p.split == 1) __syncthreads();
+        else cluster_sync();
+        if (ok && first < rows && first < count) {
+            const int64_t stride = static_cast<int64_t>(rows) * p.split * p.N;
 #pragma unroll 1
-            for (int m0 = rank + EP * set * p.split; m0 < live; m0 += SETS * EP * p.split) {
-                const int nm = imin(EP, (live - m0 + p.split - 1) / p.split);
-                const uint32_t from = base + 4 * FW_BN * m0;
-                float v[EP];
+            for (int k = first; k < count; k += rows * U) {
+                const int row = rank + k * p.split, nu = imin(U, (count - k + rows - 1) / rows);
+                float4 v[U];
 #pragma unroll
-                for (int t = 0; t < EP; ++t) {
-                    float x[FW_MAX_SPLIT];
+                for (int u = 0; u < U; ++u) {
+                    const float *at = sums + (row + u * rows * p.split) * FW_BN + 4 * qd;
+                    v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (u >= nu) continue;
+                    if (p.split == 1) v[u] = *reinterpret_cast<const float4 *>(at);
+                    else {
+                        float4 x[FW_MAX_SPLIT];
 #pragma unroll
-                    for (int r = 0; r < FW_MAX_SPLIT; ++r) {
-                        x[r] = 0.0f;
-                        if (t < nm && r < p.split) x[r] = ld_dsmem(mapa_shared(from + 4 * FW_BN * p.split * t, r));
+                        for (int r = 0; r < FW_MAX_SPLIT; ++r) {
+                            x[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (r < p.split) x[r] = ld_dsmem4(mapa_shared(smem_u32(at), r));
+                        }
+                        v[u] = x[0];
+#pragma unroll
+                        for (int r = 1; r < FW_MAX_SPLIT; ++r) {
+                            v[u].x += x[r].x;
+                            v[u].y += x[r].y;
+                            v[u].z += x[r].z;
+                            v[u].w += x[r].w;
+                        }
                     }
-                    v[t] = x[0];
-#pragma unroll
-                    for (int r = 1; r < FW_MAX_SPLIT; ++r) v[t] += x[r];
                 }
-                ep_column<OUT, EP>(ep, p.out, static_cast<int64_t>(r0 + m0) * p.N + n, static_cast<int64_t>(p.N) * p.split, nm,
-                               alpha, step, v, bias);
+                ep_quads<OUT, U>(ep, p.out, static_cast<int64_t>(r0 + row) * p.N + n0 + 4 * qd, stride, nu, alpha, step, v, bias);
             }
+        }
         __syncwarp();
-        cluster_sync();                                       // nobody reads this CTA's shared memory any more
+        if (p.split > 1) cluster_sync();                      // nobody reads this CTA's shared memory any more
     }
     tc_fence_before();
     __syncthreads();
@@ -357,11 +451,11 @@ __global__ void __launch_bounds__(FW_THREADS, 1)
     if (warp == 1) tmem_dealloc(tmem, GM_TMEM_COLS);
 }
 
-template <int FMT, int OUT, int NX>
+template <int FMT, int OUT, int NX, bool PLAIN>
 static int launch_few_nx(const CUtensorMap &tw, const CUtensorMap &tx, const FewParams &p, const EpParams &ep, int smem,
                       cudaStream_t s)
 {
-    if (ensure_dyn_smem<k_gemm_few<FMT, OUT, NX>>(FW_SMEM_MAX + 1024) != QFP4_OK) return QFP4_ERR_CUDA;
+    if (ensure_dyn_smem<k_gemm_few<FMT, OUT, NX, PLAIN>>(FW_SMEM_MAX + 1024) != QFP4_OK) return QFP4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.tiles_n * ((p.M + FW_ROWS - 1) / FW_ROWS) * p.split), 1, 1);
     cfg.blockDim = dim3(FW_THREADS, 1, 1);
@@ -376,7 +470,7 @@ static int launch_few_nx(const CUtensorMap &tw, const CUtensorMap &tx, const Few
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, k_gemm_few<FMT, OUT, NX>, tw, tx, p, ep) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, k_gemm_few<FMT, OUT, NX, PLAIN>, tw, tx, p, ep) != cudaSuccess) {
         (void)cudaGetLastError();
         return QFP4_ERR_CUDA;
     }
@@ -388,8 +482,12 @@ template <int FMT, int OUT>
 static int launch_few(const CUtensorMap &tw, const CUtensorMap &tx, const FewParams &p, const EpParams &ep, int smem,
                       cudaStream_t s)
 {
-    return p.rows <= 32 ? launch_few_nx<FMT, OUT, 1>(tw, tx, p, ep, smem, s)
-                        : launch_few_nx<FMT, OUT, 4>(tw, tx, p, ep, smem, s);
+    const bool plain = p.aligned && p.split == 1 && p.N > 4 * FW_BN && !ep.drop.on;
+    if (p.rows <= 32)
+        return plain ? launch_few_nx<FMT, OUT, 1, true>(tw, tx, p, ep, smem, s)
+                     : launch_few_nx<FMT, OUT, 1, false>(tw, tx, p, ep, smem, s);
+    return plain ? launch_few_nx<FMT, OUT, 4, true>(tw, tx, p, ep, smem, s)
+                 : launch_few_nx<FMT, OUT, 4, false>(tw, tx, p, ep, smem, s);
 }
 
 static int64_t gemm_few_tiles(int64_t M, int64_t N)
@@ -399,8 +497,8 @@ static int64_t gemm_few_tiles(int64_t M, int64_t N)
 
 // Up to 128 rows, and more where one tile an SM takes all of them: the pair
 // kernel then has too few 256 x 256 tiles, and a prepass (512 x 4096 x 4096
-// MXFP4 with bias and SiLU 18.2 us there, 14.3 here; 300 x 520 x 2080 16.7 and
-// 12.1).  Larger outputs are the pair kernel's, which reads half the operand
+// MXFP4 with bias and SiLU 18.2 us there, 13.2 here; 300 x 520 x 2080 16.7 and
+// 10.2).  Larger outputs are the pair kernel's, which reads half the operand
 // bytes from L2 for the same output.
 static bool gemm_few_fits(int64_t M, int64_t N) { return M <= FW_ROWS || gemm_few_tiles(M, N) <= 148; }
 
@@ -428,7 +526,7 @@ static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float
     const int stage = (FW_BN + p.rows) * GM_BKB;
     const int per = (p.KT + p.split - 1) / p.split;
     p.stages = imax(2, imin(imin(FW_MAX_STAGES, per), FW_SMEM_MAX / stage));
-    const int smem = imax(imax(p.stages * stage, p.split > 1 ? p.rows * FW_BN * 4 : 0), FW_SMEM_MIN) + 1024;
+    const int smem = imax(p.stages * stage, FW_SMEM_MIN) + 1024;
     CUtensorMap tw, tx;
     const uint64_t row_bytes = static_cast<uint64_t>(fmt == QFP4_MXFP8 ? K : K / 2);
     {

@@ -95,6 +95,14 @@ def test_gemm_epilogue_binary32_out(M, N, K, fmt):
     check_gemm(M, N, K, fmt, F32, bias=F32, act="silu", preact=True, p=0.1, residual=F32, step=(1 << 40) + 5)
 
 
+@pytest.mark.parametrize("M,N,K", [(1443, 16, 4192), (700, 8, 96), (2264, 136, 1312), (131, 120, 32), (1027, 392, 352)])
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_gemm_epilogue_narrow_outputs(M, N, K, fmt):
+    """Many rows of few columns; scale rows that start on any byte."""
+    check_gemm(M, N, K, fmt, BF, bias=F32, act="gelu", preact=True, p=0.25, residual=F32, step=9)
+    check_gemm(M, N - 4, K, fmt, F32, bias=BF, residual=BF)
+
+
 @pytest.mark.parametrize("act", list(ACT))
 @pytest.mark.parametrize("M", [2, 70, 300])
 def test_gemm_epilogue_activations(act, M):
