@@ -245,12 +245,6 @@ __device__ __forceinline__ float ld_as_float(const void *p, int f32, int64_t i)
     return f32 ? static_cast<const float *>(p)[i]
                : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
 }
-__device__ __forceinline__ float2 ld2_as_float(const void *p, int f32, int64_t i)   // i even
-{
-    if (f32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
-    return make_float2(bf16lo(w), bf16hi(w));
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -283,7 +277,7 @@ __device__ __forceinline__ void st_v8(void *p, const uint32_t *r)
 
 // Sixteen consecutive values of one row, as loaded: binary32 in r[0 .. 15],
 // bf16 pairs in r[0 .. 7].  nc < 16 (a multiple of 4): the row's last ones.
-struct Row16 {
+struct alignas(16) Row16 {
     uint32_t r[16];
 };
 __device__ __forceinline__ void row16_load(Row16 &v, const void *p, int f32, int64_t i, int nc, int wide)

@@ -69,7 +69,8 @@ template <int OUT, int U>
 __device__ __forceinline__ void ep_quads(const EpParams &ep, void *out, int64_t i0, int64_t stride, int nu, float alpha,
                                          uint64_t step, const float4 *acc, float4 bias)
 {
-    float res[4 * U], v[4 * U];
+    alignas(16) float res[4 * U];
+    float v[4 * U];
     if (ep.residual)
 #pragma unroll
         for (int u = 0; u < U; ++u)
