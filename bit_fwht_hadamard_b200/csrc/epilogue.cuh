@@ -86,17 +86,18 @@ __device__ __forceinline__ void drop_values(const DropParams &d, uint64_t step, 
 // All in binary32 on the unrounded sum z.  A NaN stays a NaN in each of them.
 //
 // GELU on pairs of values, from the normal distribution function of the
-// negative half line: with a = |z| and E = e^(-a^2/2),
-//   Phi(-a) = E m(a),   GELU(z)  = max(z, 0) - a Phi(-a),
-//   Phi(-a) - a phi(a) = E t(a),   GELU'(z) = 1/2 + sign(z) (1/2 - E t(a)).
-// m (Mills' ratio over sqrt(2 pi)) and t = m - a / sqrt(2 pi) are smooth; each
-// is a polynomial of degree 10, fitted on [0, 6] by least squares weighted by
-// E with the weights raised towards the largest error.  E m and E t are then
-// within 1.1e-7 everywhere (a E m within 3.4e-7): E outruns the polynomials
-// beyond 6, and at 16, where a is cut off, it is 2.6e-56, that is 0.  One
-// special-function instruction and five packed multiply-adds a value; erff
-// takes about 50 instructions (the GEMM's GELU epilogue took 311 us with it at
-// 8192 x 11008 x 4096, 215 us with a polynomial).  A NaN stays one.
+// negative half line, so that nothing cancels there: with a = |z| and
+// E = e^(-a^2/2),
+//   Phi(-a) = E m(a),   GELU(z) = max(z, 0) - a Phi(-a).
+// m (Mills' ratio over sqrt(2 pi)) falls like 1 / a.  As t P(t), t = 1 / (1 +
+// 0.34 a), with P of degree 8 (fitted on [0, 14] by least squares of the
+// relative error, its weights raised towards the largest) it keeps its digits
+// on the whole half line: within 5.1 u as evaluated, u = 2^-24, so that
+// GELU(z) for z < 0 is within (12 + 1.25 z^2) u of itself (the rounded
+// exponent's share), down to 2^-126 where E ends.  Two special-function
+// instructions and ten packed multiply-adds a pair.  A polynomial in a, of
+// degree 10 and weighted by E, was as accurate in absolute terms only: 23 % off
+// at -5, eleven times too large at -6.  A NaN stays one.
 __device__ __forceinline__ float abs_upto(float x, float most)
 {
     float r;
@@ -115,6 +116,12 @@ __device__ __forceinline__ float exp2_fast(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // E of a pair
 __device__ __forceinline__ uint64_t gauss2(uint64_t a)
 {
@@ -122,23 +129,32 @@ __device__ __forceinline__ uint64_t gauss2(uint64_t a)
     f2unpack(f2mul(f2mul(a, f2pack(-0.721347520f, -0.721347520f)), a), x, y);   // -a^2 / 2 log2 e
     return f2pack(exp2_fast(x), exp2_fast(y));
 }
+// m of a pair, a >= 0
+__device__ __forceinline__ uint64_t mills2(uint64_t a)
+{
+    float x, y;
+    f2unpack(f2fma(a, f2pack(0.34f, 0.34f), f2pack(1.0f, 1.0f)), x, y);
+    const uint64_t t = f2pack(rcp_fast(x), rcp_fast(y));
+    uint64_t p = f2pack(-0.026120467f, -0.026120467f);
+    p = f2fma(p, t, f2pack(0.13949946f, 0.13949946f));
+    p = f2fma(p, t, f2pack(-0.27313268f, -0.27313268f));
+    p = f2fma(p, t, f2pack(0.20218259f, 0.20218259f));
+    p = f2fma(p, t, f2pack(-0.0447184f, -0.0447184f));
+    p = f2fma(p, t, f2pack(0.11535914f, 0.11535914f));
+    p = f2fma(p, t, f2pack(0.115197666f, 0.115197666f));
+    p = f2fma(p, t, f2pack(0.1361122f, 0.1361122f));
+    p = f2fma(p, t, f2pack(0.1356205f, 0.1356205f));
+    return f2mul(p, t);
+}
 __device__ __forceinline__ uint64_t gelu2(float z0, float z1)
 {
     const uint64_t a = f2pack(abs_upto(z0, 16.0f), abs_upto(z1, 16.0f));
     const uint64_t na = f2mul(a, f2pack(-1.0f, -1.0f));
-    uint64_t p = f2pack(1.63168431e-06f, 1.63168431e-06f);
-    p = f2fma(p, a, f2pack(-3.52076859e-05f, -3.52076859e-05f));
-    p = f2fma(p, a, f2pack(0.000339737744f, 0.000339737744f));
-    p = f2fma(p, a, f2pack(-0.00197462458f, -0.00197462458f));
-    p = f2fma(p, a, f2pack(0.00793938432f, 0.00793938432f));
-    p = f2fma(p, a, f2pack(-0.0243139211f, -0.0243139211f));
-    p = f2fma(p, a, f2pack(0.0611548796f, 0.0611548796f));
-    p = f2fma(p, a, f2pack(-0.132513791f, -0.132513791f));
-    p = f2fma(p, a, f2pack(0.249916792f, 0.249916792f));
-    p = f2fma(p, a, f2pack(-0.39893651f, -0.39893651f));
-    p = f2fma(p, a, f2pack(0.49999994f, 0.49999994f));
-    return f2fma(f2mul(na, gauss2(a)), p, f2pack(max0_nan(z0), max0_nan(z1)));
+    return f2fma(f2mul(na, gauss2(a)), mills2(a), f2pack(max0_nan(z0), max0_nan(z1)));
 }
+// The slope, E t(a) with t = m - a / sqrt(2 pi): GELU'(z) = 1/2 + sign(z)
+// (1/2 - E t(a)), t a polynomial of degree 10 fitted on [0, 6] weighted by E
+// (E t within 1.1e-7).
 __device__ __forceinline__ uint64_t gelu_slope2(float z0, float z1)
 {
     const uint64_t a = f2pack(abs_upto(z0, 16.0f), abs_upto(z1, 16.0f));
