@@ -152,29 +152,19 @@ __device__ __forceinline__ uint64_t gelu2(float z0, float z1)
     const uint64_t na = f2mul(a, f2pack(-1.0f, -1.0f));
     return f2fma(f2mul(na, gauss2(a)), mills2(a), f2pack(max0_nan(z0), max0_nan(z1)));
 }
-// The slope, E t(a) with t = m - a / sqrt(2 pi): GELU'(z) = 1/2 + sign(z)
-// (1/2 - E t(a)), t a polynomial of degree 10 fitted on [0, 6] weighted by E
-// (E t within 1.1e-7).
+// The slope from the same m: Phi(-a) - a phi(a) = E t, t = m - a / sqrt(2 pi),
+// is the slope at -a, and 1 - E t the one at a, so that the negative side
+// keeps its digits here too (E t within (20 + 1.25 a^2) u of its two terms' sum;
+// a polynomial for t weighted by E, and 1/2 + sign(z) (1/2 - E t), was within
+// 1.2e-7 whatever the slope.  The epilogue's backward pass, 8192 x 11008 bf16:
+// 98 us with that, 101 with this one).
 __device__ __forceinline__ uint64_t gelu_slope2(float z0, float z1)
 {
     const uint64_t a = f2pack(abs_upto(z0, 16.0f), abs_upto(z1, 16.0f));
-    uint64_t p = f2pack(1.63168431e-06f, 1.63168431e-06f);
-    p = f2fma(p, a, f2pack(-3.52076859e-05f, -3.52076859e-05f));
-    p = f2fma(p, a, f2pack(0.000339737744f, 0.000339737744f));
-    p = f2fma(p, a, f2pack(-0.00197462458f, -0.00197462458f));
-    p = f2fma(p, a, f2pack(0.00793938432f, 0.00793938432f));
-    p = f2fma(p, a, f2pack(-0.0243139211f, -0.0243139211f));
-    p = f2fma(p, a, f2pack(0.0611548796f, 0.0611548796f));
-    p = f2fma(p, a, f2pack(-0.132513791f, -0.132513791f));
-    p = f2fma(p, a, f2pack(0.249916792f, 0.249916792f));
-    p = f2fma(p, a, f2pack(-0.797878802f, -0.797878802f));
-    p = f2fma(p, a, f2pack(0.49999994f, 0.49999994f));
-    float x, y;
-    f2unpack(f2fma(f2mul(gauss2(a), f2pack(-1.0f, -1.0f)), p, f2pack(0.5f, 0.5f)), x, y);   // >= -0.13
-    // times the sign of z
-    x = __uint_as_float(__float_as_uint(x) ^ (__float_as_uint(z0) & 0x80000000u));
-    y = __uint_as_float(__float_as_uint(y) ^ (__float_as_uint(z1) & 0x80000000u));
-    return f2add(f2pack(x, y), f2pack(0.5f, 0.5f));
+    const uint64_t t = f2fma(a, f2pack(-0.39894228f, -0.39894228f), mills2(a));
+    const uint64_t up = f2pack(z0 >= 0.0f ? 1.0f : 0.0f, z1 >= 0.0f ? 1.0f : 0.0f);
+    const uint64_t sign = f2fma(up, f2pack(-2.0f, -2.0f), f2pack(1.0f, 1.0f));
+    return f2fma(f2mul(gauss2(a), t), sign, up);
 }
 
 // x within [-most, most]; a NaN stays one.

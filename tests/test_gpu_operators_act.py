@@ -73,3 +73,14 @@ def test_activation_keeps_the_tail(name):
     show((got - want).abs(), bound, z, got, want, name)
     got = forward(z, name, torch.bfloat16).double()
     show((got - want).abs(), bound + 2.0 ** -8 * (1 + 2.0 ** -6) * want.abs(), z, got, want, name + " bf16")
+
+
+@pytest.mark.parametrize("name", ["gelu"])
+def test_slope_keeps_the_tail(name):
+    z = grid()
+    z = z[:z.numel() // 8 * 8].view(1, -1)
+    _, want, e, _, mag = parts(z.double(), name)
+    # the other factors' words and products behind the tail's; six of the result where the sigmoid is near one
+    bound = (e + 8) * U * mag + 6 * U * torch.where(z > 0, want.abs(), 0 * want) + TINY
+    got, _ = q.epilogue_backward(torch.ones_like(z), z, act=ACT[name])
+    show((got.double() - want).abs().view(-1), bound.view(-1), z.view(-1), got.view(-1), want.view(-1), name)
