@@ -177,14 +177,56 @@ __device__ __forceinline__ float clamp_nan(float x, float most)
     return r;
 }
 
-// 1 / (1 + e^-x); 0 for x -> -inf (the fast division gives 0 for a huge
-// divisor), 1 for x -> inf.
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// The sigmoid f of a pair of x and g = 1 - f, from E = e^-|x| <= 1 and r = 1 /
+// (1 + E): r and E r are the two, so neither loses digits where it is small
+// (1 / (1 + e^-x) from the fast exponential was 95 u off at x = -80, and 1 - f had
+// no digit left beyond x = 17), and no divisor is ever large.
+struct Sigmoid2 {
+    uint64_t E, r;
 
-// GELU's tanh form: 1/2 (1 + tanh t) = sigmoid(2 t)
-__device__ __forceinline__ float gelu_tanh_arg(float z)
+    __device__ __forceinline__ void finish()
+    {
+        float x, y;
+        f2unpack(f2add(E, f2pack(1.0f, 1.0f)), x, y);
+        r = f2pack(rcp_fast(x), rcp_fast(y));
+    }
+    // f of the pair whose signs are z0's and z1's
+    __device__ __forceinline__ uint64_t f(float z0, float z1) const
+    {
+        float x, y;
+        f2unpack(E, x, y);
+        return f2mul(f2pack(z0 >= 0.0f ? 1.0f : x, z1 >= 0.0f ? 1.0f : y), r);
+    }
+    // z f g
+    __device__ __forceinline__ uint64_t zfg(uint64_t z) const { return f2mul(f2mul(z, r), f2mul(E, r)); }
+};
+// E from both words of |x| log2 e: the rounding of the first, up to 2^-18 of E,
+// comes back as 1 - ln 2 times it.
+__device__ __forceinline__ Sigmoid2 sigmoid2(float x0, float x1)
 {
-    return z * fmaf(0.071354816f * z, z, 1.5957691216f);   // 2 sqrt(2/pi) (z + 0.044715 z^3)
+    const uint64_t a = f2pack(abs_upto(x0, 128.0f), abs_upto(x1, 128.0f));
+    const uint64_t n = f2mul(a, f2pack(-1.44269502f, -1.44269502f));
+    const uint64_t over =
+        f2fma(a, f2pack(1.92596303e-08f, 1.92596303e-08f), f2fma(a, f2pack(1.44269502f, 1.44269502f), n));
+    float x, y;
+    f2unpack(n, x, y);
+    Sigmoid2 s;
+    s.E = f2mul(f2pack(exp2_fast(x), exp2_fast(y)),
+                f2fma(over, f2pack(-0.693147182f, -0.693147182f), f2pack(1.0f, 1.0f)));
+    s.finish();
+    return s;
+}
+// GELU's tanh form: 1/2 (1 + tanh t) is the sigmoid of x = 2 t = 2 sqrt(2/pi) (z
+// + 0.044715 z^3), here times log2 e.  (x is rounded already: no second word.)
+__device__ __forceinline__ Sigmoid2 sigmoid_tanh2(float z0, float z1)
+{
+    const uint64_t z = f2pack(z0, z1);
+    float x, y;
+    f2unpack(f2mul(z, f2fma(f2mul(z, f2pack(0.102943234f, 0.102943234f)), z, f2pack(2.30220819f, 2.30220819f))), x, y);
+    Sigmoid2 s;
+    s.E = f2pack(exp2_fast(-fabsf(x)), exp2_fast(-fabsf(y)));
+    s.finish();
+    return s;
 }
 
 // In place on an even number of values; act is the same for every thread.
@@ -202,11 +244,13 @@ __device__ __forceinline__ void act_forward(float *v, int act)
         break;
     case QFP4_ACT_GELU_TANH:
 #pragma unroll
-        for (int t = 0; t < N; ++t) v[t] = v[t] * sigmoid_fast(gelu_tanh_arg(v[t]));
+        for (int t = 0; t < N; t += 2)
+            f2unpack(f2mul(f2pack(v[t], v[t + 1]), sigmoid_tanh2(v[t], v[t + 1]).f(v[t], v[t + 1])), v[t], v[t + 1]);
         break;
     case QFP4_ACT_SILU:
 #pragma unroll
-        for (int t = 0; t < N; ++t) v[t] = v[t] * sigmoid_fast(v[t]);
+        for (int t = 0; t < N; t += 2)
+            f2unpack(f2mul(f2pack(v[t], v[t + 1]), sigmoid2(v[t], v[t + 1]).f(v[t], v[t + 1])), v[t], v[t + 1]);
         break;
     default: break;
     }
@@ -227,18 +271,24 @@ __device__ __forceinline__ void act_backward(float *d, const float *z, int act)
             f2unpack(f2mul(f2pack(d[t], d[t + 1]), gelu_slope2(z[t], z[t + 1])), d[t], d[t + 1]);
         break;
     case QFP4_ACT_GELU_TANH:
-        // beyond |z| = 80 the slope is 0 or 1 to binary32; the clamp keeps z^3 and the products finite
+        // f + x f g 2 sqrt(2/pi) (1 + 3 0.044715 x^2); beyond |z| = 80 the slope is
+        // 0 or 1 to binary32: the clamp keeps z^3 and the products finite
 #pragma unroll
-        for (int t = 0; t < N; ++t) {
-            const float x = clamp_nan(z[t], 80.0f), f = sigmoid_fast(gelu_tanh_arg(x));
-            d[t] *= fmaf(x * f * (1.0f - f), fmaf(0.214064448f * x, x, 1.5957691216f), f);
+        for (int t = 0; t < N; t += 2) {
+            const float x0 = clamp_nan(z[t], 80.0f), x1 = clamp_nan(z[t + 1], 80.0f);
+            const Sigmoid2 s = sigmoid_tanh2(x0, x1);
+            const uint64_t x = f2pack(x0, x1);
+            const uint64_t k = f2fma(f2mul(x, f2pack(0.214064449f, 0.214064449f)), x, f2pack(1.59576917f, 1.59576917f));
+            f2unpack(f2mul(f2pack(d[t], d[t + 1]), f2fma(s.zfg(x), k, s.f(x0, x1))), d[t], d[t + 1]);
         }
         break;
     case QFP4_ACT_SILU:
+        // f + z f g
 #pragma unroll
-        for (int t = 0; t < N; ++t) {
-            const float f = sigmoid_fast(z[t]);
-            d[t] *= f * fmaf(z[t], 1.0f - f, 1.0f);
+        for (int t = 0; t < N; t += 2) {
+            const Sigmoid2 s = sigmoid2(z[t], z[t + 1]);
+            const uint64_t k = f2add(s.zfg(f2pack(z[t], z[t + 1])), s.f(z[t], z[t + 1]));
+            f2unpack(f2mul(f2pack(d[t], d[t + 1]), k), d[t], d[t + 1]);
         }
         break;
     default: break;

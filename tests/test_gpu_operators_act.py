@@ -11,6 +11,8 @@ import operators_ref as R
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 TINY = 2.0 ** -120                                           # results below this may be flushed to zero
+# E = e^-|x| (e^(-z^2/2) for GELU) may be flushed below 2^-126.  For a slope that is f (1 + z g x'), f, g <= 1, it takes
+# 2^-126 (1 + |z| x') with it: up to 2^-118 for the tanh form, whose x' is 23 at z = -10, where E = 2^-126.
 ACT = {n: i for i, n in enumerate(R.ACTS)}
 
 
@@ -22,8 +24,9 @@ def grid():
 
 
 def parts(z, name):
-    """(act, slope, relative error of the tail factor in u): the sigmoid or
-    normal distribution function behind each, without cancellation."""
+    """(act, slope, relative error of the tail factor in u, the terms' sizes, what a
+    flushed E takes of the slope): the sigmoid or normal distribution function
+    behind each, without cancellation."""
     if name == "gelu":
         # Phi(-a) = E m(a), E = 2^y with y = -a^2/2 log2 e after two roundings and a rounded constant (1.25 a^2 u of E),
         # 2^x 4 u, m within 6 u, two products
@@ -31,7 +34,7 @@ def parts(z, name):
         pdf = torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5
         e = 1.25 * z * z + 12
         small = 0.5 * torch.special.erfc(z.abs() / 2 ** 0.5)
-        return z * phi, phi + z * pdf, e, (z * small).abs(), small + z.abs() * pdf
+        return z * phi, phi + z * pdf, e, (z * small).abs(), small + z.abs() * pdf, TINY
     if name == "silu":
         # the exponent to both its words: 2^x 4 u, correction 2 u, 1 + E, reciprocal 2 u, two products
         x, dx, e = z, torch.ones_like(z), torch.full_like(z, 12.0)
@@ -43,7 +46,8 @@ def parts(z, name):
     f, g = torch.sigmoid(x), torch.sigmoid(-x)
     small = torch.minimum(f, g)
     # f itself rounds as the tail where it is the small one, and to 4 u where it is near one
-    return z * f, f + z * f * g * dx, e, (z * small).abs(), small + z.abs() * f * g * dx
+    flushed = 2.0 ** -126 * (1 + z.abs() * dx)
+    return z * f, f + z * f * g * dx, e, (z * small).abs(), small + z.abs() * f * g * dx, flushed
 
 
 def show(err, bound, z, got, want, name):
@@ -62,11 +66,11 @@ def forward(z, name, dt):
     return q.gemm_epilogue(A, B, 1, n, 0, q.MXFP4, bias=z, act=ACT[name], out_dtype=dt)[0][0]
 
 
-@pytest.mark.parametrize("name", ["gelu"])
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh", "silu"])
 def test_activation_keeps_the_tail(name):
     z = grid()
     z = z[:z.numel() // 8 * 8]
-    want, _, e, tail, _ = parts(z.double(), name)
+    want, _, e, tail, _, _ = parts(z.double(), name)
     # the tail's own roundings, and four of the result (GELU's one, the sigmoid near one and its product)
     bound = e * U * tail + 4 * U * torch.where(z > 0, want.abs(), 0 * want) + TINY
     got = forward(z, name, torch.float32).double()
@@ -75,12 +79,12 @@ def test_activation_keeps_the_tail(name):
     show((got - want).abs(), bound + 2.0 ** -8 * (1 + 2.0 ** -6) * want.abs(), z, got, want, name + " bf16")
 
 
-@pytest.mark.parametrize("name", ["gelu"])
+@pytest.mark.parametrize("name", ["gelu", "gelu_tanh", "silu"])
 def test_slope_keeps_the_tail(name):
     z = grid()
     z = z[:z.numel() // 8 * 8].view(1, -1)
-    _, want, e, _, mag = parts(z.double(), name)
+    _, want, e, _, mag, flushed = parts(z.double(), name)
     # the other factors' words and products behind the tail's; six of the result where the sigmoid is near one
-    bound = (e + 8) * U * mag + 6 * U * torch.where(z > 0, want.abs(), 0 * want) + TINY
+    bound = (e + 8) * U * mag + 6 * U * torch.where(z > 0, want.abs(), 0 * want) + flushed
     got, _ = q.epilogue_backward(torch.ones_like(z), z, act=ACT[name])
     show((got.double() - want).abs().view(-1), bound.view(-1), z.view(-1), got.view(-1), want.view(-1), name)
