@@ -136,7 +136,11 @@ constexpr int EB_TILE = 32;                                   // vectors of a bl
 constexpr int EB_BLOCKS = 4, EB_WAVE = 4;
 
 // Grid of the kernel: column tiles, row chunks (each a multiple of eight
-// rows) for at most EB_WAVE blocks an SM, so that all run at once.
+// rows) for at most EB_WAVE blocks an SM, so that all run at once; several
+// times as many where a lane would add more than SUM_TERMS rows one after the
+// other (with terms of one sign the error of such a sum grows with its length:
+// 16000 of them were 2e-4 off).
+constexpr int SUM_TERMS = 2048;
 struct EbGrid {
     int tiles, chunks;
     int64_t rows;
@@ -146,7 +150,9 @@ static EbGrid epilogue_backward_grid(int64_t M, int64_t N, int V)
     EbGrid g;
     const int64_t tw = EB_TILE * V;
     g.tiles = static_cast<int>((N % V ? N + V - 1 : N) / tw + ((N % V ? N + V - 1 : N) % tw != 0));
-    const int64_t want = imax<int64_t>(1, imin<int64_t>(EB_WAVE * 148 / g.tiles, 512));
+    const int64_t wave = imax<int64_t>(1, imin<int64_t>(EB_WAVE * 148 / g.tiles, 512));
+    const int64_t waves = (M + wave * 8 * SUM_TERMS - 1) / (wave * 8 * SUM_TERMS);
+    const int64_t want = imin<int64_t>(wave * waves, 65535 / wave * wave);      // blockIdx.y
     g.rows = ((M + want - 1) / want + 7) / 8 * 8;
     g.chunks = static_cast<int>((M + g.rows - 1) / g.rows);
     return g;
