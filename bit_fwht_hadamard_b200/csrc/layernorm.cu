@@ -683,11 +683,13 @@ static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
         p.gamma_sm = p.G < 1024 || (LNB_SMEM - 4 * D) / stage >= 3;
         p.stages = static_cast<int>(imin<int64_t>(8, (LNB_SMEM - (p.gamma_sm ? 4 * D : 0)) / stage));
     }
-    if (p.stages) {
-        p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, 148);
-    } else if (p.G) {
-        // blocks for 1024 threads an SM, but no more than there are rows
-        p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, 148 * (1024 / (p.G * p.GR)));
+    if (p.G) {
+        // one block an SM, or blocks for 1024 threads an SM, but no more than
+        // there are rows; several waves of them where a group would add more
+        // than SUM_TERMS rows one after the other
+        const int64_t wave = p.stages ? 148 : 148 * (1024 / (p.G * p.GR));
+        const int64_t waves = (M + wave * p.GR * SUM_TERMS - 1) / (wave * p.GR * SUM_TERMS);
+        p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, wave * waves);
     } else {
         const int64_t cols = (D + 255) / 256;
         const int64_t want = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));

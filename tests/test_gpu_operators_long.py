@@ -18,3 +18,17 @@ def test_bias_gradient_of_many_rows(M, N):
     _, db = q.epilogue_backward(dy, out={"dZ": dy})
     want = M * float(torch.tensor(C))
     assert float((db.double() - want).abs().max()) <= TERMS * want
+
+
+# three odd columns, the ring of bulk copies
+@pytest.mark.parametrize("M,D", [(1 << 26, 3), (9_800_000, 520)])
+def test_norm_gradients_of_many_rows(M, D):
+    dy = torch.full((M, D), C, device="cuda")
+    row = torch.linspace(0.5, 1.5, D, device="cuda")
+    x = row.expand(M, D).contiguous()
+    zero, one = torch.zeros(M, device="cuda"), torch.ones(M, device="cuda")
+    _, dg, db = q.layernorm_backward(dy, x, None, zero, one, want_dx=False)
+    want = M * float(torch.tensor(C))
+    assert float((db.double() - want).abs().max()) <= TERMS * want
+    assert float(((dg.double() - want * row.double()) / (want * row.double())).abs().max()) <= TERMS + 2 * U
+    assert q.qfp4_last_device_error() == 0
