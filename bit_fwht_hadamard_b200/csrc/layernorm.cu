@@ -692,7 +692,10 @@ static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
         p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, wave * waves);
     } else {
         const int64_t cols = (D + 255) / 256;
-        const int64_t want = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));
+        // chunks for eight blocks an SM, and as many times more as keep a
+        // chunk's running sum to SUM_TERMS rows
+        const int64_t wave = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));
+        const int64_t want = wave * ((M + wave * SUM_TERMS - 1) / (wave * SUM_TERMS));
         p.rows = (M + want - 1) / want;
         p.parts = (M + p.rows - 1) / p.rows;
     }

@@ -20,8 +20,8 @@ def test_bias_gradient_of_many_rows(M, N):
     assert float((db.double() - want).abs().max()) <= TERMS * want
 
 
-# three odd columns, the ring of bulk copies
-@pytest.mark.parametrize("M,D", [(1 << 26, 3), (9_800_000, 520)])
+# three odd columns, the ring of bulk copies, rows longer than any group
+@pytest.mark.parametrize("M,D", [(1 << 26, 3), (9_800_000, 520), (80000, 65536)])
 def test_norm_gradients_of_many_rows(M, D):
     dy = torch.full((M, D), C, device="cuda")
     row = torch.linspace(0.5, 1.5, D, device="cuda")
