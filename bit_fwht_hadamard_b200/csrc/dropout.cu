@@ -130,7 +130,7 @@ static int column_sums(const float *partial, int64_t rows, int64_t N, int TW, in
 // element.  Reads dY and Z once, writes dZ once: bound by memory, with half of
 // the issue slots taken by GELU's slope.  One wave of blocks, so that each
 // keeps its columns' sums over many rows and few partial rows are left: 8192 x
-// 11008 bf16 with GELU 101 us (83 from memory alone), some 20 more with several
+// 11008 bf16 with GELU 98 us (83 from memory alone), some 20 more with several
 // waves.
 constexpr int EB_TILE = 32;                                   // vectors of a block's column tile
 constexpr int EB_BLOCKS = 4, EB_WAVE = 4;

@@ -89,15 +89,20 @@ __device__ __forceinline__ void drop_values(const DropParams &d, uint64_t step, 
 // negative half line, so that nothing cancels there: with a = |z| and
 // E = e^(-a^2/2),
 //   Phi(-a) = E m(a),   GELU(z) = max(z, 0) - a Phi(-a).
-// m (Mills' ratio over sqrt(2 pi)) falls like 1 / a.  As t P(t), t = 1 / (1 +
-// 0.34 a), with P of degree 8 (fitted on [0, 14] by least squares of the
-// relative error, its weights raised towards the largest) it keeps its digits
-// on the whole half line: within 5.1 u as evaluated, u = 2^-24, so that
-// GELU(z) for z < 0 is within (12 + 1.25 z^2) u of itself (the rounded
-// exponent's share), down to 2^-126 where E ends.  Two special-function
-// instructions and ten packed multiply-adds a pair.  A polynomial in a, of
-// degree 10 and weighted by E, was as accurate in absolute terms only: 23 % off
-// at -5, eleven times too large at -6.  A NaN stays one.
+// m (Mills' ratio over sqrt(2 pi)) falls like 1 / a: a quotient of polynomials
+// of degree 3 and 4 keeps its digits on the whole half line.  All their terms
+// are positive; they were fitted on [0, 13.4] by least squares of the relative
+// error over 1.5 + 0.6 a^2, the weights raised towards the largest (u = 2^-24:
+// within (1.1 + 0.43 a^2) u; a rounding a step, the coefficients', the reciprocal
+// and the product at most 12 u more).  E is within (4 + 1.05 a^2) u (its rounded
+// exponent), so GELU(z) for z < 0 is within (19 + 1.5 z^2) u of itself, down to
+// 2^-126 where E ends; on a dense grid it was within (12 + 1.25 z^2) u.  Two
+// special-function instructions a value, nine packed multiply-adds a pair.  A
+// polynomial in a of degree 10, weighted by E, took as long (8192 x 11008 x 4096
+// NVFP4 with bias, GELU and z kept 212 us, this one 210) but was accurate in
+// absolute terms only: 23 % off at -5, eleven times too large at -6.  1 / (1 +
+// 0.34 a) times a polynomial of degree 8 in it is as accurate as the quotient,
+// with a longer chain (backward pass 102 us, the quotient 98).  A NaN stays one.
 __device__ __forceinline__ float abs_upto(float x, float most)
 {
     float r;
@@ -132,19 +137,18 @@ __device__ __forceinline__ uint64_t gauss2(uint64_t a)
 // m of a pair, a >= 0
 __device__ __forceinline__ uint64_t mills2(uint64_t a)
 {
+    uint64_t n = f2pack(0.0144826053f, 0.0144826053f);
+    n = f2fma(n, a, f2pack(0.108570509f, 0.108570509f));
+    n = f2fma(n, a, f2pack(0.342697442f, 0.342697442f));
+    n = f2fma(n, a, f2pack(0.49999997f, 0.49999997f));
+    uint64_t d = f2pack(0.0363141261f, 0.0363141261f);
+    d = f2fma(d, a, f2pack(0.271760285f, 0.271760285f));
+    d = f2fma(d, a, f2pack(0.900663376f, 0.900663376f));
+    d = f2fma(d, a, f2pack(1.48327541f, 1.48327541f));
+    d = f2fma(d, a, f2pack(1.0f, 1.0f));
     float x, y;
-    f2unpack(f2fma(a, f2pack(0.34f, 0.34f), f2pack(1.0f, 1.0f)), x, y);
-    const uint64_t t = f2pack(rcp_fast(x), rcp_fast(y));
-    uint64_t p = f2pack(-0.026120467f, -0.026120467f);
-    p = f2fma(p, t, f2pack(0.13949946f, 0.13949946f));
-    p = f2fma(p, t, f2pack(-0.27313268f, -0.27313268f));
-    p = f2fma(p, t, f2pack(0.20218259f, 0.20218259f));
-    p = f2fma(p, t, f2pack(-0.0447184f, -0.0447184f));
-    p = f2fma(p, t, f2pack(0.11535914f, 0.11535914f));
-    p = f2fma(p, t, f2pack(0.115197666f, 0.115197666f));
-    p = f2fma(p, t, f2pack(0.1361122f, 0.1361122f));
-    p = f2fma(p, t, f2pack(0.1356205f, 0.1356205f));
-    return f2mul(p, t);
+    f2unpack(d, x, y);
+    return f2mul(n, f2pack(rcp_fast(x), rcp_fast(y)));
 }
 __device__ __forceinline__ uint64_t gelu2(float z0, float z1)
 {
@@ -154,10 +158,9 @@ __device__ __forceinline__ uint64_t gelu2(float z0, float z1)
 }
 // The slope from the same m: Phi(-a) - a phi(a) = E t, t = m - a / sqrt(2 pi),
 // is the slope at -a, and 1 - E t the one at a, so that the negative side
-// keeps its digits here too (E t within (20 + 1.25 a^2) u of its two terms' sum;
+// keeps its digits here too (E t within (19 + 1.5 a^2) u of its two terms' sum;
 // a polynomial for t weighted by E, and 1/2 + sign(z) (1/2 - E t), was within
-// 1.2e-7 whatever the slope.  The epilogue's backward pass, 8192 x 11008 bf16:
-// 98 us with that, 101 with this one).
+// 1.2e-7 whatever the slope, and took as long).
 __device__ __forceinline__ uint64_t gelu_slope2(float z0, float z1)
 {
     const uint64_t a = f2pack(abs_upto(z0, 16.0f), abs_upto(z1, 16.0f));

@@ -28,11 +28,12 @@ def parts(z, name):
     flushed E takes of the slope): the sigmoid or normal distribution function
     behind each, without cancellation."""
     if name == "gelu":
-        # Phi(-a) = E m(a), E = 2^y with y = -a^2/2 log2 e after two roundings and a rounded constant (1.25 a^2 u of E),
-        # 2^x 4 u, m within 6 u, two products
+        # Phi(-a) = E m(a): E = 2^y, y = -a^2/2 log2 e after two roundings and a rounded constant, (4 + 1.05 a^2) u;
+        # m = N(a) / D(a), positive terms of degree 3 and 4: the quotient's own fit (1.1 + 0.43 a^2) u, a rounding a step
+        # and the coefficients' (4 u and 5 u), two for the reciprocal, one for the product; two more products
         phi = 0.5 * torch.special.erfc(-z / 2 ** 0.5)
         pdf = torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5
-        e = 1.25 * z * z + 12
+        e = 1.48 * z * z + 19.1
         small = 0.5 * torch.special.erfc(z.abs() / 2 ** 0.5)
         return z * phi, phi + z * pdf, e, (z * small).abs(), small + z.abs() * pdf, TINY
     if name == "silu":
