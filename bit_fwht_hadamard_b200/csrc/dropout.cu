@@ -150,7 +150,7 @@ static EbGrid epilogue_backward_grid(int64_t M, int64_t N, int V)
     EbGrid g;
     const int64_t tw = EB_TILE * V;
     g.tiles = static_cast<int>((N % V ? N + V - 1 : N) / tw + ((N % V ? N + V - 1 : N) % tw != 0));
-    const int64_t wave = imax<int64_t>(1, imin<int64_t>(EB_WAVE * 148 / g.tiles, 512));
+    const int64_t wave = imax<int64_t>(1, imin<int64_t>(EB_WAVE * SMS / g.tiles, 512));
     const int64_t waves = (M + wave * 8 * SUM_TERMS - 1) / (wave * 8 * SUM_TERMS);
     const int64_t want = imin<int64_t>(wave * waves, 65535 / wave * wave);      // blockIdx.y
     g.rows = ((M + want - 1) / want + 7) / 8 * 8;

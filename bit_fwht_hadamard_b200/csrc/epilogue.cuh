@@ -6,6 +6,10 @@
 
 namespace qfp4 {
 
+// SMs that grids and workspaces are sized for.  A constant, where num_sms() asks
+// the device: a workspace query needs no device, and its call must agree with it.
+constexpr int SMS = 148;
+
 // ------------------------------------------------------------------ dropout
 // Element e stays iff word e mod 4 of Philox4x32-10, keyed on the 64-bit seed
 // at counter (e / 4, 2^63 + step), is >= threshold = floor(p 2^32); it is then

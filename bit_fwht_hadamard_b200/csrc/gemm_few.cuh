@@ -501,7 +501,7 @@ static int64_t gemm_few_tiles(int64_t M, int64_t N)
 // MXFP4 with bias and SiLU 18.2 us there, 13.2 here; 300 x 520 x 2080 16.7 and
 // 10.2).  Larger outputs are the pair kernel's, which reads half the operand
 // bytes from L2 for the same output.
-static bool gemm_few_fits(int64_t M, int64_t N) { return M <= FW_ROWS || gemm_few_tiles(M, N) <= 148; }
+static bool gemm_few_fits(int64_t M, int64_t N) { return M <= FW_ROWS || gemm_few_tiles(M, N) <= SMS; }
 
 static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float *A_tscale, const uint8_t *B_codes,
                     const uint8_t *B_scales, const float *B_tscale, int64_t M, int64_t N, int64_t K, qfp4_fmt fmt,
@@ -522,7 +522,7 @@ static int gemm_few(const uint8_t *A_codes, const uint8_t *A_scales, const float
     p.out = out;
     // as many CTAs as there are SMs, by splitting K (a CTA keeps two k-tiles at least)
     const int64_t tiles = gemm_few_tiles(M, N);
-    p.split = static_cast<int>(imax<int64_t>(1, imin<int64_t>(imin<int64_t>(FW_MAX_SPLIT, 148 / tiles), p.KT / 2)));
+    p.split = static_cast<int>(imax<int64_t>(1, imin<int64_t>(imin<int64_t>(FW_MAX_SPLIT, SMS / tiles), p.KT / 2)));
     // all of a CTA's k-tiles under way at once, where shared memory allows
     const int stage = (FW_BN + p.rows) * GM_BKB;
     const int per = (p.KT + p.split - 1) / p.split;

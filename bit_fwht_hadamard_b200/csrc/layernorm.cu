@@ -8,10 +8,11 @@
 //
 // Bound by memory: each call reads its matrices once and writes its result
 // once.  A row lies in the registers of the group of threads that takes it
-// (a warp, or a block of 128 to 1024), in vectors of 16 bytes where the rows
-// start on 16 bytes and element by element where they do not, so the second
-// pass of the variance (on x - mean, which keeps a large mean from cancelling)
-// costs no second read.  Longer rows are read again from the caches.
+// (a warp, or a block of 64 to 1024), so the second pass of the variance (on x -
+// mean, which keeps a large mean from cancelling) costs no second read: in
+// vectors of 16 bytes where the rows start on 16 bytes; where they do not,
+// element by element up to 4096 columns, beyond that in vectors aligned in memory
+// (forward).  Longer rows are read again from the caches.
 #include "vec.cuh"
 
 namespace qfp4 {
@@ -247,7 +248,7 @@ static int layernorm_vectors(const LnForward &a)
 {
     constexpr int V = ln_v<DT>();
     const int64_t nv = a.D / V;
-    if (a.M <= 2 * 148) {
+    if (a.M <= 2 * SMS) {
         if (nv <= 32) return launch_layernorm<DT, V, 32, 1, 1, false>(a);
         if (nv <= 128) return launch_layernorm<DT, V, 128, 1, 1, false>(a);
         if (nv <= 512) return launch_layernorm<DT, V, 512, 1, 1, false>(a);
@@ -267,7 +268,7 @@ static int layernorm_vectors(const LnForward &a)
 template <int DT>
 static int layernorm_elements(const LnForward &a)
 {
-    if (a.M <= 2 * 148) {
+    if (a.M <= 2 * SMS) {
         if (a.D <= 1024) return launch_layernorm<DT, 1, 128, 8, 1, false>(a);
         return launch_layernorm<DT, 1, 1024, 4, 1, false>(a);
     }
@@ -687,14 +688,14 @@ static LnPlan layernorm_backward_plan(int64_t M, int64_t D, bool f32)
         // one block an SM, or blocks for 1024 threads an SM, but no more than
         // there are rows; several waves of them where a group would add more
         // than SUM_TERMS rows one after the other
-        const int64_t wave = p.stages ? 148 : 148 * (1024 / (p.G * p.GR));
+        const int64_t wave = p.stages ? SMS : SMS * (1024 / (p.G * p.GR));
         const int64_t waves = (M + wave * p.GR * SUM_TERMS - 1) / (wave * p.GR * SUM_TERMS);
         p.parts = imin<int64_t>((M + p.GR - 1) / p.GR, wave * waves);
     } else {
         const int64_t cols = (D + 255) / 256;
         // chunks for eight blocks an SM, and as many times more as keep a
         // chunk's running sum to SUM_TERMS rows
-        const int64_t wave = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * 148 + cols - 1) / cols));
+        const int64_t wave = imax<int64_t>(1, imin<int64_t>(imin<int64_t>(M, 512), (8 * SMS + cols - 1) / cols));
         const int64_t want = wave * ((M + wave * SUM_TERMS - 1) / (wave * SUM_TERMS));
         p.rows = (M + want - 1) / want;
         p.parts = (M + p.rows - 1) / p.rows;

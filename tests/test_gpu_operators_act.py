@@ -29,8 +29,8 @@ def parts(z, name):
     behind each, without cancellation."""
     if name == "gelu":
         # Phi(-a) = E m(a): E = 2^y, y = -a^2/2 log2 e after two roundings and a rounded constant, (4 + 1.05 a^2) u;
-        # m = N(a) / D(a), positive terms of degree 3 and 4: the quotient's own fit (1.1 + 0.43 a^2) u, a rounding a step
-        # and the coefficients' (4 u and 5 u), two for the reciprocal, one for the product; two more products
+        # m = N(a) / D(a), positive terms of degree 3 and 4: the quotient's own fit (1.1 + 0.43 a^2) u, a rounding a
+        # step and the coefficients' (4 u and 5 u), two for the reciprocal, one for the product; two more products
         phi = 0.5 * torch.special.erfc(-z / 2 ** 0.5)
         pdf = torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5
         e = 1.48 * z * z + 19.1
