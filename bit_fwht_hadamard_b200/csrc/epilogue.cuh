@@ -263,7 +263,7 @@ __device__ __forceinline__ void act_forward(float *v, int act)
     }
 }
 
-// d[t] *= act'(z[t]) on N values (N even).
+// d[t] *= act'(z[t]) on N values (N even).  (ReLU's slope at a NaN is 0.)
 template <int N>
 __device__ __forceinline__ void act_backward(float *d, const float *z, int act)
 {
@@ -411,8 +411,8 @@ __device__ __forceinline__ float4 bias4_load(const EpParams &ep, int col, int nc
 // A lane has a row and works on sixteen columns at a time, whole 32-byte
 // sectors: 8192 x 11008 x 4096 NVFP4 with bias, GELU and z kept took 693 us on
 // the plain product's fragments (two columns a lane, one element at a time),
-// 322 a lane a row, 220 with GELU's polynomial and the bias staged (256 in a
-// sustained loop, under the power cap; the product alone 194).
+// 322 a lane a row (with erff), 215 with GELU as above and the bias staged (255 in
+// a sustained loop, under the power cap; with the bias alone 182).
 //
 // The last step of qfp4_gemm_epilogue on the accumulators acc[0 .. 15] of one
 // row's columns col .. col + 15 (the first nc of them exist; nc and col are
